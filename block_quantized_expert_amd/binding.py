@@ -29,7 +29,9 @@ EXPORTED = ["moe_route", "moe_route_hash", "moe_route_group", "moe_group_workspa
             "moe_forward_single_kernel", "moe_forward_workspace_init", "moe_forward",
             "moe_forward_timed", "moe_forward_noalloc", "moe_status_string",
             "moe_stream_read", "moe_mfma_rate", "moe_mfma_rate_out_floats", "moe_route_ex", "moe_route_group_ex", "moe_ffn_forward_ex",
-            "moe_forward_ex", "moe_packed_experts_bytes", "moe_pack_experts"]
+            "moe_forward_ex", "moe_packed_experts_bytes", "moe_pack_experts",
+            "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
+            "moe_route_backward", "moe_quantize_int8", "moe_product_int8", "moe_swiglu_int8"]
 
 WEIGHT_TYPES = {"mxfp4": MOE_W_MXFP4, "fp8_e4m3_b128": MOE_W_FP8E4M3_B128}
 
@@ -73,6 +75,11 @@ class MoeLayer(ctypes.Structure):
                 ("has_shared", ctypes.c_int32), ("shared_inter", ctypes.c_int32),
                 ("shared_gate", MoeProj), ("shared_up", MoeProj), ("shared_down", MoeProj),
                 ("packed_experts", ctypes.c_void_p)]
+
+
+class MoeInt8Weight(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 _lib = None
@@ -135,6 +142,19 @@ def lib() -> ctypes.CDLL:
         L.moe_packed_experts_bytes.restype = S
         L.moe_pack_experts.argtypes = [ctypes.POINTER(MoeLayer), P, S, P]
         L.moe_stream_read.restype = ctypes.c_int
+        D, W = ctypes.c_int64, ctypes.POINTER(MoeInt8Weight)
+        L.moe_dispatch.argtypes = [P, I, D, I, I, I, I, P, P, P, D, P]
+        L.moe_dispatch_backward.argtypes = [P, I, D, I, I, I, P, P, D, P]
+        L.moe_combine.argtypes = [P, I, D, I, I, I, P, P, P, D, P, I, D, P]
+        L.moe_combine_backward.argtypes = [P, I, D, P, I, D, I, I, I, I, P, P, P, P, D, P, P]
+        L.moe_route_backward.argtypes = [P, P, P, I, I, I, F, P, P, P]
+        L.moe_quantize_int8.argtypes = [P, I, D, I, I, P, P, P]
+        L.moe_product_int8.argtypes = [W, P, P, I, P, P, I, P, I, D, P]
+        L.moe_swiglu_int8.argtypes = [W, W, P, P, I, P, P, I, P, I, D, P]
+        for name in ("moe_dispatch", "moe_dispatch_backward", "moe_combine",
+                     "moe_combine_backward", "moe_route_backward", "moe_quantize_int8",
+                     "moe_product_int8", "moe_swiglu_int8"):
+            getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -512,3 +532,279 @@ def moe_forward_ex(layer: Layer, logits, x, opts, routed_scale=1.5,
                                 _opts_ref(opts), _ptr(x), x_type, n, *buffers.args(),
                                 _stream(stream), *evs), "moe_forward_ex")
     return buffers
+
+
+# ----------------------------------------------------------------------------
+# Rows in expert order, gradients of routing (moe_rows.h) and products in 8-bit
+# integers (moe_int8.h).  These calls check dtypes, shapes and layouts of their
+# tensors (ValueError) on top of the library's own checks; outputs that are
+# not given are allocated on the call's stream.
+# ----------------------------------------------------------------------------
+
+_ACT_TYPES = {torch.float32: MOE_ACT_F32, torch.bfloat16: MOE_ACT_BF16}
+
+
+def _act_type(t, name):
+    """moe_act_type of a tensor's dtype."""
+    code = _ACT_TYPES.get(t.dtype if isinstance(t, torch.Tensor) else t)
+    if code is None:
+        raise ValueError("%s must be float32 or bfloat16" % name)
+    return code
+
+
+def _rows_arg(t, name, shape, dev):
+    """A matrix whose rows may be strided; returns its row stride."""
+    if t.dim() != 2 or t.shape != shape:
+        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != dev:
+        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
+    n, c = shape
+    if (c > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < c):
+        raise ValueError("%s: rows must be contiguous and must not overlap" % name)
+    return t.stride(0) if n > 1 else c
+
+
+def _dense_arg(t, name, dtype, numel, dev):
+    """A contiguous tensor of the dtype with numel elements."""
+    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.device != dev:
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s"
+                         % (name, dtype, numel, dev))
+    return t
+
+
+class _on:
+    """The device and stream a call runs on: tensors made inside belong to
+    that stream.  ``handle`` is the stream for the library."""
+
+    __slots__ = ("stream", "handle", "guard")
+
+    def __init__(self, dev, stream):
+        if dev.type != "cuda":
+            raise ValueError("tensors must be on the GPU, got %s" % dev)
+        current = torch.cuda.current_stream(dev)
+        self.stream = current if stream is None else stream
+        self.handle = self.stream.cuda_stream
+        self.guard = None
+        if self.stream != current or dev.index != torch.cuda.current_device():
+            self.guard = torch.cuda.stream(self.stream)
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+def _grouping_args(grouping, n_slots, dev):
+    counts, offsets, perm, inv_perm = grouping
+    n_experts = offsets.numel() - 1
+    _dense_arg(offsets, "offsets", torch.int32, n_experts + 1, dev)
+    for t, name in ((perm, "perm"), (inv_perm, "inv_perm")):
+        _dense_arg(t, name, torch.int32, max(n_slots, t.numel() if n_slots == 0 else 0), dev)
+    return n_experts, offsets.data_ptr(), perm.data_ptr(), inv_perm.data_ptr()
+
+
+def moe_dispatch(x, grouping, top_k, rows=None, stream=None):
+    """Rows [n*top_k][hidden] in expert order; those that no slot has are 0."""
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    n, h = x.shape
+    ty = _act_type(x, "x")
+    xs = _rows_arg(x, "x", (n, h), dev)
+    e, off, _, inv = _grouping_args(grouping, n * top_k, dev)
+    with _on(dev, stream) as st:
+        if rows is None:
+            rows = torch.empty((n * top_k, h), dtype=x.dtype, device=dev)
+        elif rows.dtype != x.dtype:
+            raise ValueError("rows must have x's dtype")
+        rs = _rows_arg(rows, "rows", (n * top_k, h), dev)
+        _check(lib().moe_dispatch(x.data_ptr(), ty, xs, n, top_k, h, e, off, inv,
+                                  rows.data_ptr(), rs, st), "moe_dispatch")
+    return rows
+
+
+def moe_dispatch_backward(drows, grouping, top_k, dx=None, stream=None):
+    """dx [n][hidden]: the sum of a token's rows."""
+    dev = drows.device
+    if drows.dim() != 2 or top_k <= 0 or drows.shape[0] % top_k:
+        raise ValueError("drows must be a matrix of n*top_k rows")
+    slots, h = drows.shape
+    n = slots // top_k
+    ty = _act_type(drows, "drows")
+    rs = _rows_arg(drows, "drows", (slots, h), dev)
+    _, _, _, inv = _grouping_args(grouping, slots, dev)
+    with _on(dev, stream) as st:
+        if dx is None:
+            dx = torch.empty((n, h), dtype=drows.dtype, device=dev)
+        elif dx.dtype != drows.dtype:
+            raise ValueError("dx must have drows' dtype")
+        ds = _rows_arg(dx, "dx", (n, h), dev)
+        _check(lib().moe_dispatch_backward(drows.data_ptr(), ty, rs, n, top_k, h, inv,
+                                           dx.data_ptr(), ds, st), "moe_dispatch_backward")
+    return dx
+
+
+def moe_combine(rows, w, grouping, base=None, y=None, y_dtype=None, stream=None):
+    """y [n][hidden] = base + the weighted sum of each token's rows.  y is of
+    its own dtype, base's, y_dtype or rows' (the first that is given)."""
+    dev = rows.device
+    if rows.dim() != 2 or w.dim() != 2 or rows.shape[0] != w.numel():
+        raise ValueError("rows must be [n*top_k][hidden] and w [n][top_k]")
+    n, k = w.shape
+    h = rows.shape[1]
+    ty = _act_type(rows, "rows")
+    rs = _rows_arg(rows, "rows", (n * k, h), dev)
+    _dense_arg(w, "w", torch.float32, n * k, dev)
+    _, _, _, inv = _grouping_args(grouping, n * k, dev)
+    with _on(dev, stream) as st:
+        if y is None:
+            y_dtype = base.dtype if base is not None else (y_dtype or rows.dtype)
+            y = torch.empty((n, h), dtype=y_dtype, device=dev)
+        yt = _act_type(y, "y")
+        ys = _rows_arg(y, "y", (n, h), dev)
+        bs = 0
+        if base is not None:
+            if base.dtype != y.dtype:
+                raise ValueError("base must have y's dtype")
+            bs = _rows_arg(base, "base", (n, h), dev)
+        _check(lib().moe_combine(rows.data_ptr(), ty, rs, n, k, h, w.data_ptr(), inv,
+                                 None if base is None else base.data_ptr(), bs, y.data_ptr(), yt,
+                                 ys, st), "moe_combine")
+    return y
+
+
+def moe_combine_backward(dy, rows, w, grouping, drows=None, dw=None, stream=None):
+    """(drows [n*top_k][hidden] of rows' dtype, dw fp32 [n][top_k])."""
+    dev = rows.device
+    if rows.dim() != 2 or w.dim() != 2 or rows.shape[0] != w.numel():
+        raise ValueError("rows must be [n*top_k][hidden] and w [n][top_k]")
+    n, k = w.shape
+    h = rows.shape[1]
+    ty, yt = _act_type(rows, "rows"), _act_type(dy, "dy")
+    rs = _rows_arg(rows, "rows", (n * k, h), dev)
+    ds = _rows_arg(dy, "dy", (n, h), dev)
+    _dense_arg(w, "w", torch.float32, n * k, dev)
+    e, off, _, inv = _grouping_args(grouping, n * k, dev)
+    with _on(dev, stream) as st:
+        if drows is None:
+            drows = torch.empty((n * k, h), dtype=rows.dtype, device=dev)
+        elif drows.dtype != rows.dtype:
+            raise ValueError("drows must have rows' dtype")
+        if dw is None:
+            dw = torch.empty((n, k), dtype=torch.float32, device=dev)
+        _dense_arg(dw, "dw", torch.float32, n * k, dev)
+        os_ = _rows_arg(drows, "drows", (n * k, h), dev)
+        _check(lib().moe_combine_backward(dy.data_ptr(), yt, ds, rows.data_ptr(), ty, rs, n, k, h,
+                                          e, w.data_ptr(), off, inv, drows.data_ptr(), os_,
+                                          dw.data_ptr(), st), "moe_combine_backward")
+    return drows, dw
+
+
+def moe_route_backward(logits, ids, dw, routed_scale=1.5, dlogits=None, dev_error=None,
+                       stream=None):
+    """dlogits fp32 [n][n_experts] of the learned router's weights."""
+    dev = logits.device
+    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
+        raise ValueError("logits must be [n][n_experts] and ids [n][top_k]")
+    n, e = logits.shape
+    k = ids.shape[1]
+    _dense_arg(logits, "logits", torch.float32, n * e, dev)
+    _dense_arg(ids, "ids", torch.int32, n * k, dev)
+    _dense_arg(dw, "dw", torch.float32, n * k, dev)
+    with _on(dev, stream) as st:
+        if dlogits is None:
+            dlogits = torch.empty((n, e), dtype=torch.float32, device=dev)
+        _dense_arg(dlogits, "dlogits", torch.float32, n * e, dev)
+        if dev_error is not None:
+            _dense_arg(dev_error, "dev_error", torch.int32, 1, dev)
+        _check(lib().moe_route_backward(logits.data_ptr(), ids.data_ptr(), dw.data_ptr(), n, e, k,
+                                        routed_scale, dlogits.data_ptr(),
+                                        None if dev_error is None else dev_error.data_ptr(), st),
+               "moe_route_backward")
+    return dlogits
+
+
+class Int8Weight:
+    """A moe_int8_weight over device tensors (kept alive): ``q`` int8
+    [n_experts][rows][cols] or [rows][cols], ``scale`` fp32 of q's shape
+    without cols."""
+
+    def __init__(self, q, scale):
+        if q.dim() == 2:
+            q, scale = q.unsqueeze(0), scale.unsqueeze(0)
+        if q.dim() != 3 or q.dtype != torch.int8 or not q.is_contiguous():
+            raise ValueError("q must be a contiguous int8 tensor of two or three dimensions")
+        _dense_arg(scale, "scale", torch.float32, q.shape[0] * q.shape[1], q.device)
+        self.q, self.scale = q, scale
+        self.c = MoeInt8Weight(q.shape[0], q.shape[1], q.shape[2], q.data_ptr(),
+                               scale.data_ptr())
+        self.ref = ctypes.byref(self.c)
+
+    @property
+    def rows(self):
+        return self.c.rows
+
+
+def moe_quantize_int8(x, q=None, scale=None, stream=None):
+    """(q int8 [n][cols], scale fp32 [n]) with x ~ q * scale."""
+    dev = x.device
+    if x.dim() != 2:
+        raise ValueError("x must be a matrix")
+    n, c = x.shape
+    ty = _act_type(x, "x")
+    xs = _rows_arg(x, "x", (n, c), dev)
+    with _on(dev, stream) as st:
+        if q is None:
+            q = torch.empty((n, c), dtype=torch.int8, device=dev)
+        if scale is None:
+            scale = torch.empty(n, dtype=torch.float32, device=dev)
+        _dense_arg(q, "q", torch.int8, n * c, dev)
+        _dense_arg(scale, "scale", torch.float32, n, dev)
+        _check(lib().moe_quantize_int8(x.data_ptr(), ty, xs, n, c, q.data_ptr(),
+                                       scale.data_ptr(), st), "moe_quantize_int8")
+    return q, scale
+
+
+def _int8_call(name, weights, q, scale, grouping, top_k, out_dtype, out, stream):
+    w = weights[0]
+    dev = q.device
+    if q.dim() != 2 or q.shape[1] != w.c.cols:
+        raise ValueError("q must be [rows][%d]" % w.c.cols)
+    _dense_arg(q, "q", torch.int8, q.numel(), dev)
+    _dense_arg(scale, "scale", torch.float32, q.shape[0], dev)
+    if w.q.device != dev:
+        raise ValueError("the weights are on %s, q is on %s" % (w.q.device, dev))
+    n = q.shape[0] * (top_k or 1)
+    off = perm = None
+    if grouping is not None:
+        e, off, perm, _ = _grouping_args(grouping, n, dev)
+        if e != w.c.n_experts:
+            raise ValueError("the grouping has %d experts, the weights %d" % (e, w.c.n_experts))
+    with _on(dev, stream) as st:
+        if out is None:
+            out = torch.empty((n, w.c.rows), dtype=out_dtype, device=dev)
+        ot = _act_type(out, "out")
+        os_ = _rows_arg(out, "out", (n, w.c.rows), dev)
+        _check(getattr(lib(), name)(*[v.ref for v in weights], q.data_ptr(), scale.data_ptr(), n,
+                                    off, perm, top_k, out.data_ptr(), ot, os_, st), name)
+    return out
+
+
+def moe_product_int8(weight, q, scale, grouping=None, top_k=0, out_dtype=torch.bfloat16, out=None,
+                     stream=None):
+    """out [slots][rows]: q (int8 [n][cols], a scale a row) times the weight's
+    rows.  With a grouping, rows of q in expert order (top_k 0) or tokens
+    (top_k > 0: every slot's token is gathered)."""
+    return _int8_call("moe_product_int8", (weight,), q, scale, grouping, top_k, out_dtype, out,
+                      stream)
+
+
+def moe_swiglu_int8(gate, up, q, scale, grouping=None, top_k=0, out_dtype=torch.bfloat16,
+                    out=None, stream=None):
+    """SwiGLU of the gate and up products; arguments as moe_product_int8."""
+    return _int8_call("moe_swiglu_int8", (gate, up), q, scale, grouping, top_k, out_dtype, out,
+                      stream)

@@ -1,0 +1,268 @@
+"""Rounding to int8 and the int8 products against 64-bit references.
+
+Bounds: q and the scales are exact (the scale is one fp32 division).  The
+int32 sum is exact; turned to fp32 and multiplied by two scales it is off by
+three half-steps of fp32, then half a step of the output's type.  SwiGLU's
+quotient g / (1 + e^-g) has condition number 1 + |g| in g; the exponential
+(4 half-steps), the sum, the quotient and the last product come on top, and u
+brings its own three."""
+
+import numpy as np
+import pytest
+import torch
+
+from block_quantized_expert_amd import binding as B
+from rows_testlib import (U32, assert_within, group, half_step, int8_weight, make_ids, normal,
+                          on_gpu, product_ref, quantize_ref, strided)
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    B.lib()
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,c,pad", [(1, 16, 0), (1, 4096, 0), (3, 48, 1), (17, 2064, 7),
+                                     (130, 1024, 0), (5, 65536, 0), (2, 8208, 3),
+                                     (700, 4096, 0)])
+def test_quantize_is_exact(n, c, pad, dtype):
+    print("case quantize", n, c, pad, dtype, flush=True)
+    x = normal(n + c, n, c)
+    x[:, ::97] *= 12
+    x = x.to(dtype)
+    # exact halves and values right beside them: fractions (m + 1/2) / 127 of
+    # the largest value, which is a multiple of 127 here
+    x[0] = 0
+    halves = torch.arange(0, min(c - 1, 127), dtype=torch.float32) + 0.5
+    x[0, 1:1 + halves.numel()] = halves * 2
+    x[0, 0] = 254
+    q, s = B.moe_quantize_int8(strided(x.cuda(), pad))
+    rq, rs = quantize_ref(x.double().numpy())
+    assert np.array_equal(q.cpu().numpy(), rq)
+    assert np.array_equal(s.cpu().numpy(), rs)
+
+
+def test_quantize_borders_in_fp32():
+    # values one fp32 step around every border of a row whose largest value
+    # makes the borders inexact
+    for top in (1.0, 3.1415927, 1e-20, 7e30, 3e-39, 1.0000001):
+        a = np.float32(top)
+        border = ((np.arange(-127, 127) + 0.5) / 127 * np.float64(a)).astype(np.float32)
+        v = np.concatenate([[a], border, np.nextafter(border, np.float32(np.inf)),
+                            np.nextafter(border, np.float32(-np.inf))]).astype(np.float32)
+        v = np.clip(np.resize(v, 768), -a, a)
+        q, s = B.moe_quantize_int8(torch.from_numpy(v).reshape(1, -1).cuda())
+        rq, rs = quantize_ref(v.reshape(1, -1))
+        assert np.array_equal(q.cpu().numpy(), rq), top
+        assert np.array_equal(s.cpu().numpy(), rs), top
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_zero_and_non_finite_rows(dtype):
+    x = normal(1, 6, 64, dtype=dtype)
+    x[1] = 0.0
+    x[2] = -0.0
+    x[3, 5] = float("inf")
+    x[4, 63] = float("nan")
+    x[5, 0] = float("-inf")
+    x[5, 1] = float("nan")
+    q, s = (t.cpu().numpy() for t in B.moe_quantize_int8(x.cuda()))
+    rq, rs = quantize_ref(x[:3].double().numpy())
+    assert np.array_equal(q[:3], rq) and np.array_equal(s[:3], rs)
+    assert not q[1:].any()
+    assert np.array_equal(s[1:3], np.zeros(2, np.float32)) and np.isnan(s[3:]).all()
+
+
+def _bound(ref, dtype, steps):
+    err = steps * U32 * np.abs(ref) * (1 + 2.0 ** -20)
+    return err + half_step(dtype) * (np.abs(ref) + err) + 2.0 ** -149
+
+
+def _swiglu(g, u):
+    y = g / (1 + np.exp(-g)) * u
+    return y, 3 * (1 + np.abs(g)) + 4 + 1 + 1 + 3 + 1
+
+
+def _left(n, cols, seed):
+    rng = np.random.default_rng(seed)
+    return (rng.integers(-128, 128, (n, cols), dtype=np.int8),
+            rng.uniform(0.01, 0.03, n).astype(np.float32))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,rows,cols,pad", [
+    (1, 1, 16, 0), (1, 4096, 4096, 0), (2, 33, 128, 1), (15, 16, 144, 0), (16, 17, 112, 0),
+    (17, 1235, 2064, 0), (64, 64, 512, 0), (100, 300, 1040, 5), (129, 257, 256, 0),
+    (257, 511, 528, 0), (300, 128, 65536, 0), (513, 260, 1536, 0), (1030, 1025, 640, 3)])
+def test_dense_product(n, rows, cols, pad, dtype):
+    print("case dense", n, rows, cols, pad, dtype, flush=True)
+    wq, ws = int8_weight(n + rows, 1, rows, cols)
+    q, s = _left(n, cols, 7)
+    w = B.Int8Weight(torch.from_numpy(wq[0]).cuda(), torch.from_numpy(ws[0]).cuda())
+    out = strided(torch.zeros(n, rows, dtype=dtype, device="cuda"), pad).fill_(float("nan"))
+    got = B.moe_product_int8(w, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(), out=out)
+    assert got is out
+    ref = product_ref(wq, ws, q, s, [0, n], np.arange(n))
+    assert_within(out, ref, _bound(ref, dtype, 3), "out")
+    up, us = int8_weight(n + rows + 1, 1, rows, cols)
+    u = B.Int8Weight(torch.from_numpy(up[0]).cuda(), torch.from_numpy(us[0]).cuda())
+    got = B.moe_swiglu_int8(w, u, torch.from_numpy(q).cuda(), torch.from_numpy(s).cuda(),
+                            out_dtype=dtype)
+    y, steps = _swiglu(ref, product_ref(up, us, q, s, [0, n], np.arange(n)))
+    assert_within(got, y, _bound(y, dtype, steps), "swiglu")
+
+
+# tokens, top_k, experts, experts used, share dropped, rows, cols
+GROUPED = [
+    (1, 1, 1, 1, 0.0, 16, 16),
+    (1, 6, 256, 6, 0.0, 128, 512),
+    (7, 3, 5, 3, 0.3, 40, 176),
+    (32, 6, 256, 120, 0.0, 64, 256),
+    (33, 2, 1024, 60, 0.2, 19, 128),
+    (100, 4, 16, 7, 0.1, 130, 272),
+    (150, 8, 8, 8, 0.0, 260, 128),     # every expert takes every token
+    (333, 3, 4, 3, 0.25, 100, 640),
+    (40, 2, 64, 2, 0.0, 256, 1024),    # two crowded experts, the rest empty
+    (60, 4, 12, 12, 1.0, 48, 64),      # no slot has an expert
+    (700, 2, 6, 5, 0.05, 320, 384),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,k,e,used,drop,rows,cols", GROUPED)
+def test_grouped_products(n, k, e, used, drop, rows, cols, dtype):
+    print("case grouped", n, k, e, used, drop, rows, cols, dtype, flush=True)
+    ids = make_ids(n, k, e, drop, used, seed=n + e)
+    g = group(ids, e)
+    off, perm = g[1], g[2]
+    total = int(off[-1])
+    gd = on_gpu(g)
+    (gq, gs), (uq, us) = int8_weight(n, e, rows, cols), int8_weight(n + 1, e, rows, cols)
+    gate, up = (B.Int8Weight(*on_gpu(w)) for w in ((gq, gs), (uq, us)))
+
+    # gathered tokens, SwiGLU and plain
+    q, s = _left(n, cols, 8)
+    qd, sd = on_gpu((q, s))
+    left = perm // k
+    a = product_ref(gq, gs, q, s, off, left)
+    b = product_ref(uq, us, q, s, off, left)
+    out = torch.full((n * k, rows), float("nan"), dtype=dtype, device="cuda")
+    B.moe_swiglu_int8(gate, up, qd, sd, gd, top_k=k, out=out)
+    y, steps = _swiglu(a, b)
+    assert_within(out, y, _bound(y, dtype, steps), "swiglu")
+    assert not out[total:].any()
+    out = B.moe_product_int8(gate, qd, sd, gd, top_k=k, out_dtype=dtype)
+    assert_within(out, a, _bound(a, dtype, 3), "gathered product")
+
+    # rows in expert order; those past the last expert's hold anything
+    q, s = _left(n * k, cols, 9)
+    s[total:] = np.nan
+    qd, sd = on_gpu((q, s))
+    out = torch.full((n * k, rows), float("nan"), dtype=dtype, device="cuda")
+    B.moe_product_int8(up, qd, sd, gd, out=out)
+    ref = product_ref(uq, us, q, s, off, np.arange(n * k))
+    assert_within(out, ref, _bound(ref, dtype, 3), "sorted product")
+    assert not out[total:].any()
+
+
+def test_extreme_values_sum_exactly():
+    # 65536 products of -128 * -128 and of -128 * 127: 2^30 and its like in int32
+    c = 65536
+    q = np.full((2, c), -128, np.int8)
+    w = np.stack([np.full(c, -128, np.int8), np.full(c, 127, np.int8)])
+    out = B.moe_product_int8(B.Int8Weight(*on_gpu((w, np.ones(2, np.float32)))),
+                             *on_gpu((q, np.ones(2, np.float32))), out_dtype=F32)
+    assert out.cpu().tolist() == [[float(2 ** 30), float(-128 * 127 * c)]] * 2
+
+
+def test_non_finite_scales_stay_in_their_rows():
+    wq, ws = int8_weight(3, 1, 70, 128)
+    q, s = _left(40, 128, 4)
+    s[5] = np.nan
+    q[5] = 0
+    out = B.moe_product_int8(B.Int8Weight(*on_gpu((wq, ws))), *on_gpu((q, s)), out_dtype=F32)
+    assert torch.isnan(out[5]).all()
+    keep = np.arange(40) != 5
+    ref = product_ref(wq, ws, q, s, [0, 40], np.arange(40))[keep]
+    assert_within(out[torch.from_numpy(keep).cuda()], ref, _bound(ref, F32, 3), "out")
+
+
+def test_swiglu_of_far_gates():
+    # gates of hundreds either way: SiLU is g or vanishes
+    c, rows = 64, 32
+    gq = np.full((1, rows, c), 1, np.int8)
+    q = np.stack([np.full(c, v, np.int8) for v in (-127, -20, -1, 0, 1, 20, 127)])
+    s = np.full(7, 0.25, np.float32)
+    one = np.ones((1, rows), np.float32)
+    w = B.Int8Weight(*on_gpu((gq, one)))
+    out = B.moe_swiglu_int8(w, w, *on_gpu((q, s)), out_dtype=F32)
+    a = product_ref(gq, one, q, s, [0, 7], np.arange(7))
+    y = a * np.exp(-np.logaddexp(0, -a)) * a
+    assert_within(out, y, _bound(y, F32, 3 * (1 + np.abs(a)) + 10) + 1e-30, "far gates")
+
+
+def test_no_slots():
+    w = B.Int8Weight(*on_gpu(int8_weight(1, 4, 32, 64)))
+    g = on_gpu(group(make_ids(0, 2, 4), 4))
+    q, s = torch.empty(0, 64, dtype=torch.int8, device="cuda"), torch.empty(0, device="cuda")
+    assert B.moe_product_int8(w, q, s, g, top_k=2).shape == (0, 32)
+    q, s = B.moe_quantize_int8(torch.empty(0, 64, device="cuda"))
+    assert q.shape == (0, 64) and s.shape == (0,)
+
+
+def test_left_rows_past_32_bit_offsets():
+    # 40000 rows of 65536 bytes: the last lie past 2^31; only some rows are looked at
+    n, c = 40000, 65536
+    q = torch.zeros((n, c), dtype=torch.int8, device="cuda")
+    look = torch.tensor([0, 1, 32767, 32768, 32769, 39999])
+    vals, _ = _left(6, c, 5)
+    q[look.cuda()] = torch.from_numpy(vals).cuda()
+    wq, ws = int8_weight(6, 1, 16, c)
+    out = B.moe_product_int8(B.Int8Weight(*on_gpu((wq, ws))), q,
+                             torch.ones(n, device="cuda"), out_dtype=F32)
+    ref = product_ref(wq, ws, vals, np.ones(6, np.float32), [0, 6], np.arange(6))
+    assert_within(out[look.cuda()], ref, _bound(ref, F32, 3), "out")
+    look2 = torch.ones(n, dtype=torch.bool)
+    look2[look] = False
+    assert not out[look2.cuda()].any()
+    del q, out
+    torch.cuda.empty_cache()
+
+
+def test_results_repeat_on_another_stream_and_in_a_graph():
+    n, k, e, rows, cols = 48, 4, 16, 192, 512
+    g = on_gpu(group(make_ids(n, k, e, 0.1, seed=2), e))
+    gate, up = (B.Int8Weight(*on_gpu(int8_weight(i, e, rows, cols))) for i in (1, 2))
+    x = normal(3, n, cols, dtype=BF16).cuda()
+
+    def passes(stream=None):
+        q, s = B.moe_quantize_int8(x, stream=stream)
+        h = B.moe_swiglu_int8(gate, up, q, s, g, top_k=k, stream=stream)
+        y = B.moe_product_int8(gate, q, s, g, top_k=k, out_dtype=F32, stream=stream)
+        return q, s, h, y
+
+    want = [t.clone() for t in passes()]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = passes(side)
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = passes()
+    for i in range(4):
+        x.mul_(1.25)
+        want = [t.clone() for t in passes()]
+        for t in out:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), i
