@@ -256,14 +256,337 @@ int64_t max_tiles(const ProductParams& p, int tm) {
   return n < ragged ? n : ragged;
 }
 
+// ------------------------------------------------------------- tiled products
+
+typedef __attribute__((address_space(4))) const int32_t* scalar_i32;
+
+// Sixteen bytes that a copy past the end of a row reads instead.
+__device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
+
+// Token tiles that follow one another under one strip of channels: the strip
+// is then read from memory once and by the others from L2.
+constexpr int kTileGroup = 4;
+constexpr int kTableSpan = MOE_MAX_EXPERTS / kWave + 1;
+constexpr int kGridTiled = 256;  // CUs
+
+// End of a step: this wavefront's copies into LDS are done but for the newest
+// N, its LDS reads are complete (the compiler may place the barrier above the
+// products), then the workgroup's barrier.  Not __syncthreads(), whose fence
+// would wait for every copy in flight.
+template <int N>
+__device__ __forceinline__ void step_barrier() {
+  __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4));
+  __builtin_amdgcn_s_barrier();
+}
+
+template <int TOK, int CH, int STAGES>
+struct TiledLds {
+  static constexpr int kStage = (TOK + CH) * 128;
+  static constexpr int kTable = STAGES * kStage;
+  static constexpr int kBytes = kTable + 4 * (MOE_MAX_EXPERTS + 2);
+};
+
+// Large products: TOK rows x CH rows of weights (SwiGLU: gate and up of CH / 2
+// channels) a workgroup of WT x WC wavefronts, the reduction in steps of 128
+// bytes.  Both operands go from memory into LDS by asynchronous 16-byte
+// copies, STAGES - 1 steps ahead and across the end of a tile, so a workgroup
+// that goes from tile to tile never waits for a first load; LDS also turns
+// whole 128-byte lines of memory into the matrix instruction's layout.  One
+// workgroup on a CU, 256 weight rows: two or three steps of 32 KiB of weights
+// in flight cover the latency of HBM at its full rate.  Weights are read once
+// from memory while an expert's rows fit kTileGroup tiles.
+// 4096 x 4096 x 4096: 62 us, 2.2 POP/s (a library product of the same int8
+// matrices: 67 us), bound by the matrix cores; gate and up of 4096 tokens through 256
+// experts (4.3 GB of weights): 1.23 ms, 3.5 TB/s.
+template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
+__global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductParams p) {
+  using L = TiledLds<TOK, CH, STAGES>;
+  constexpr int NW = WT * WC;
+  constexpr int CB = CH / WC / 16, TB = TOK / WT / 16;
+  constexpr int kW = CH / 8 / NW;                                // copies of weights a step
+  constexpr int kX = TOK / 8 / NW > 0 ? TOK / 8 / NW : 1;        // and of rows
+  constexpr int kStripCh = SWIGLU ? CH / 2 : CH;
+  extern __shared__ char smem[];
+  int32_t* const first = reinterpret_cast<int32_t*>(smem + L::kTable);
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r16 = lane % 16, g = lane / 16;
+  const int wt = wave % WT, wc = wave / WT;
+  const bool grouped = p.offsets != nullptr;
+  const int n_exp = grouped ? p.n_experts : 1;
+  const scalar_i32 offs = (scalar_i32)(uintptr_t)p.offsets;
+
+  auto offset_of = [&](int e) -> int {
+    if (!grouped) return e == 0 ? 0 : p.n_slots;
+    return min(max(offs[e], 0), p.n_slots);
+  };
+
+  // tiles in front of each expert's
+  if (wave == 0) {
+    int off[kTableSpan + 1], sum = 0;
+#pragma unroll
+    for (int i = 0; i <= kTableSpan; ++i) {
+      const int e = min(lane * kTableSpan + i, n_exp);
+      off[i] = grouped ? min(max(p.offsets[e], 0), p.n_slots) : (e == 0 ? 0 : p.n_slots);
+    }
+#pragma unroll
+    for (int i = 0; i < kTableSpan; ++i) sum += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
+    int incl = sum;
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) {
+      const int v = __shfl_up(incl, s);
+      if (lane >= s) incl += v;
+    }
+    int at = incl - sum;
+#pragma unroll
+    for (int i = 0; i < kTableSpan; ++i) {
+      const int e = lane * kTableSpan + i;
+      if (e <= n_exp) first[e] = at;
+      at += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
+    }
+  }
+  __syncthreads();
+  const uint32_t strips = (p.rows + kStripCh - 1) / kStripCh;
+  const uint32_t items = (uint32_t)first[n_exp] * strips;
+
+  // rows without an expert
+  if (grouped) {
+    O* out = static_cast<O*>(p.out);
+    for (int64_t r = (int64_t)offset_of(n_exp) + blockIdx.x; r < p.n_slots; r += gridDim.x)
+      for (int j = threadIdx.x; j < p.rows; j += kWave * NW)
+        out[r * p.out_stride + j] = static_cast<O>(0.0f);
+  }
+
+  // item `index`: expert, first row, rows and first channel
+  auto find = [&](uint32_t index, int& expert, int& row0, int& m, int& j0) {
+    const int t = (int)(index / strips);
+    const int a = __popcll(__ballot(first[min(lane * kTableSpan, n_exp)] <= t)) - 1;
+    const int e1 = min(a * kTableSpan + lane, n_exp);
+    const int e = a * kTableSpan + __popcll(__ballot(lane < kTableSpan && first[e1] <= t)) - 1;
+    expert = __builtin_amdgcn_readfirstlane(e);
+    const uint32_t f = __builtin_amdgcn_readfirstlane(first[expert]);
+    const uint32_t tiles = __builtin_amdgcn_readfirstlane(first[expert + 1]) - f;
+    const uint32_t rem = index - f * strips;
+    const uint32_t grp = rem / (kTileGroup * strips);
+    const uint32_t in = rem - grp * (kTileGroup * strips);
+    const uint32_t n = min((uint32_t)kTileGroup, tiles - grp * kTileGroup);
+    const int tile = grp * kTileGroup + in % n;
+    j0 = in / n * kStripCh;
+    const int lo = offset_of(expert), hi = offset_of(expert + 1);
+    row0 = lo + tile * TOK;
+    m = min(TOK, hi - row0);
+  };
+
+  // this workgroup's items: workgroup b runs on XCD b % 8, which takes one
+  // contiguous eighth of the items
+  const uint32_t xcd = blockIdx.x % 8, per = gridDim.x / 8;
+  const uint32_t end = (uint32_t)((uint64_t)items * (xcd + 1) / 8);
+  uint32_t load_item = (uint32_t)((uint64_t)items * xcd / 8) + blockIdx.x / 8;
+  uint32_t item = load_item;
+  const int ksteps = (p.cols + 127) / 128;
+  const int tail = p.cols % 128 != 0 ? ksteps - 1 : -1;
+
+  // Copies into LDS.  One copies 8 rows of 128 bytes; a lane's chunk is the
+  // one that belongs at its place: chunk c of row r lies at c ^ (r / 2 % 8),
+  // so that the 16 rows of an operand read meet different banks.
+  const char* wsrc[kW];
+  const char* xsrc[kX];
+  const int chunk_even = (lane % 8) ^ (lane / 16);  // rows 8j + lane / 8 of even j
+  int load_step = 0;
+  auto x_copy = [&](int i) { return (wave * kX + i) % (TOK / 8); };
+  auto open = [&]() {
+    int expert, row0, m, j0;
+    find(load_item, expert, row0, m, j0);
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const int j = wave * kW + i;
+      const int r = 8 * j + lane / 8;
+      const int chunk = chunk_even ^ (4 * (j & 1));
+      int ch;
+      const int8_t* w = p.w[0];
+      if (SWIGLU) {
+        const int blk = r / 16, c = blk / CB, b = blk % CB;
+        w = b < CB / 2 ? p.w[0] : p.w[1];
+        ch = j0 + (c * (CB / 2) + b % (CB / 2)) * 16 + r % 16;
+      } else {
+        ch = j0 + r;
+      }
+      wsrc[i] = reinterpret_cast<const char*>(w) +
+                ((int64_t)expert * p.rows + min(ch, p.rows - 1)) * p.cols + 16 * chunk;
+    }
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+      const int j = x_copy(i);
+      const int chunk = chunk_even ^ (4 * (j & 1));
+      int64_t row = row0 + min(8 * j + lane / 8, m - 1);
+      if (p.top_k != 0) {
+        // through the scalar cache: a vector load's wait would drain the copies in flight
+        const scalar_i32 perm = (scalar_i32)(uintptr_t)p.perm;
+        int f = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int v = perm[row0 + min(8 * j + r, m - 1)];
+          f = lane / 8 == r ? v : f;
+        }
+        row = f >= 0 && f < p.n_slots ? f / p.top_k : 0;
+      }
+      xsrc[i] = reinterpret_cast<const char*>(p.q) + row * p.cols + 16 * chunk;
+    }
+  };
+  // copies the next step into buffer b
+  auto issue = [&](int b) {
+    if (load_step == 0) open();
+    char* const buf = smem + b * L::kStage;
+    auto copy = [&](const char*& src, int lds_row, int j) {
+      const char* s = src;
+      if (load_step == tail &&
+          load_step * 128 + 16 * (chunk_even ^ (4 * (j & 1))) >= p.cols)
+        s = reinterpret_cast<const char*>(&kZeroChunk);
+      __builtin_amdgcn_global_load_lds(
+          s, (__attribute__((address_space(3))) void*)(buf + lds_row * 128), 16, 0, 0);
+      src += 128;
+    };
+#pragma unroll
+    for (int i = 0; i < kW; ++i) copy(wsrc[i], 8 * (wave * kW + i), wave * kW + i);
+#pragma unroll
+    for (int i = 0; i < kX; ++i) copy(xsrc[i], CH + 8 * x_copy(i), x_copy(i));
+    if (++load_step == ksteps) {
+      load_step = 0;
+      load_item += per;
+    }
+  };
+
+  int into = 0, from = 0, ahead = 0;
+  for (int i = 0; i < STAGES - 1; ++i)
+    if (load_item < end) {
+      issue(into);
+      into = into + 1 == STAGES ? 0 : into + 1;
+      ++ahead;
+    }
+
+  const int swz = 16 * (g ^ (r16 / 2));
+  const int woff = (wc * CB * 16 + r16) * 128 + swz;
+  const int xoff = (CH + wt * TB * 16 + r16) * 128 + swz;
+  for (; item < end; item += per) {
+    i32x4 acc[CB][TB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int t = 0; t < TB; ++t) acc[c][t] = i32x4{0, 0, 0, 0};
+    for (int ks = 0; ks < ksteps; ++ks) {
+      // this step's copies have landed and every wavefront is past the one
+      // before, whose buffer the next copies take
+      if (ahead == STAGES - 1)
+        step_barrier<(STAGES - 2) * (kW + kX)>();
+      else
+        step_barrier<0>();
+      if (load_item < end) {
+        issue(into);
+        into = into + 1 == STAGES ? 0 : into + 1;
+      } else {
+        --ahead;
+      }
+      const char* const buf = smem + from * L::kStage;
+      from = from + 1 == STAGES ? 0 : from + 1;
+      // operands two products' blocks ahead of their use
+      i32x4 wv[2][CB], xv[3];
+      auto read_w = [&](int h) {
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+          wv[h][c] = *reinterpret_cast<const i32x4*>(buf + (woff ^ (64 * h)) + c * 2048);
+      };
+      auto read_x = [&](int u) {
+        xv[u % 3] = *reinterpret_cast<const i32x4*>(buf + (xoff ^ (64 * (u / TB))) + u % TB * 2048);
+      };
+      read_w(0);
+      read_x(0);
+      read_x(1);
+#pragma unroll
+      for (int u = 0; u < 2 * TB; ++u) {
+        if (u == (TB > 2 ? TB - 2 : 0)) read_w(1);
+        if (u + 2 < 2 * TB) read_x(u + 2);
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+          acc[c][u % TB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u / TB][c], xv[u % 3],
+                                                                 acc[c][u % TB], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // lane: channels 4g .. 4g + 3 of its blocks for token r16
+    int expert, row0, m, j0;
+    find(item, expert, row0, m, j0);
+    constexpr int NB = SWIGLU ? CB / 2 : CB;
+    float sg[NB][4], su[NB][4];
+#pragma unroll
+    for (int c = 0; c < NB; ++c)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int j = min(j0 + (wc * NB + c) * 16 + 4 * g + i, p.rows - 1);
+        const int64_t s = (int64_t)expert * p.rows + j;
+        sg[c][i] = p.w_scale[0][s];
+        su[c][i] = SWIGLU ? p.w_scale[1][s] : 0.0f;
+      }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const int tok = (wt * TB + t) * 16 + r16;
+      if (tok >= m) continue;
+      const int64_t row = row0 + tok;
+      const float sx = p.scale[left_row(p, row)];
+      O* const out = static_cast<O*>(p.out) + row * p.out_stride;
+#pragma unroll
+      for (int c = 0; c < NB; ++c) {
+        const int j = j0 + (wc * NB + c) * 16 + 4 * g;
+        O v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          v[i] = static_cast<O>(finish<SWIGLU>(acc[c][t][i], acc[SWIGLU ? NB + c : c][t][i], sx,
+                                               sg[c][i], su[c][i]));
+        if (j + 4 <= p.rows) {
+          __builtin_memcpy(out + j, v, sizeof(v));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (j + i < p.rows) out[j + i] = v[i];
+        }
+      }
+    }
+  }
+}
+
+template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
+hipError_t launch_tiled(const ProductParams& p, hipStream_t stream) {
+  constexpr int lds = TiledLds<TOK, CH, STAGES>::kBytes;
+  static_assert(lds <= 160 * 1024, "LDS");
+  constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
+  static const hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kernel, dim3(kGridTiled), dim3(kWave * WT * WC), lds, stream, p);
+  return hipGetLastError();
+}
+
 template <bool SWIGLU, typename O>
-void launch_product(const ProductParams& p, hipStream_t stream) {
+hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
+  // The tile height follows the mean rows of an expert (the counts are on the
+  // device): rows of padding cost matrix time, a second tile of an expert
+  // another pass over its weights in L2.  Fewer tiles of 16 rows than twice
+  // the CUs: the direct kernel's more and smaller workgroups fill the chip
+  // better (one token through six experts: 25 us).
+  const int64_t mean = p.n_slots / p.n_experts;
   const int64_t tiles = max_tiles(p, 16);
+  const int strip = SWIGLU ? 128 : 256;
+  if (tiles * ((p.rows + strip - 1) / strip) >= 2 * kGridTiled) {
+    if (mean > 160) return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, stream);
+    if (mean > 40) return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, stream);
+    if (mean > 12) return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, stream);
+    return launch_tiled<SWIGLU, O, 16, 256, 1, 8, 4>(p, stream);
+  }
   const dim3 grid((p.rows + 15) / 16, (unsigned)(tiles < 32768 ? tiles : 32768));
   if (p.n_experts + 1 <= 5 * kWave)
     hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 5>), grid, dim3(kThreads), 0, stream, p);
   else
     hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 17>), grid, dim3(kThreads), 0, stream, p);
+  return hipGetLastError();
 }
 
 static_assert(MOE_MAX_EXPERTS + 1 <= 17 * kWave, "experts a lane of find_tile holds");
@@ -290,11 +613,12 @@ moe_status product(const moe_int8_weight* w, const moe_int8_weight* up, const in
   p.out = out;
   p.out_stride = out_stride;
   const bool bf16 = out_type == MOE_ACT_BF16;
+  hipError_t e;
   if (up != nullptr)
-    bf16 ? launch_product<true, __bf16>(p, stream) : launch_product<true, float>(p, stream);
+    e = bf16 ? launch_product<true, __bf16>(p, stream) : launch_product<true, float>(p, stream);
   else
-    bf16 ? launch_product<false, __bf16>(p, stream) : launch_product<false, float>(p, stream);
-  return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
+    e = bf16 ? launch_product<false, __bf16>(p, stream) : launch_product<false, float>(p, stream);
+  return e == hipSuccess ? MOE_OK : MOE_ERR_DEVICE;
 }
 
 }  // namespace

@@ -266,3 +266,52 @@ def test_results_repeat_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def _dense(n, rows, cols, pad, dtype):
+    wq, ws = int8_weight(n + rows, 1, rows, cols)
+    uq, us = int8_weight(n + rows + 1, 1, rows, cols)
+    q, s = _left(n, cols, 7)
+    w, u = B.Int8Weight(*on_gpu((wq, ws))), B.Int8Weight(*on_gpu((uq, us)))
+    qd, sd = on_gpu((q, s))
+    out = strided(torch.zeros(n, rows, dtype=dtype, device="cuda"), pad).fill_(float("nan"))
+    B.moe_product_int8(w, qd, sd, out=out)
+    ref = product_ref(wq, ws, q, s, [0, n], np.arange(n))
+    assert_within(out, ref, _bound(ref, dtype, 3), "out")
+    got = B.moe_swiglu_int8(w, u, qd, sd, out_dtype=dtype)
+    y, steps = _swiglu(ref, product_ref(uq, us, q, s, [0, n], np.arange(n)))
+    assert_within(got, y, _bound(y, dtype, steps), "swiglu")
+
+
+# sizes of the tiled kernels: rows of every tile height, ragged in each
+# dimension, reductions of less than one step to several
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,rows,cols,pad", [
+    (1030, 8200, 176, 3), (1024, 8192, 128, 0), (600, 8500, 64, 0), (2000, 4099, 1296, 1),
+    (200, 16500, 144, 0), (100, 20011, 272, 1), (129, 18000, 16, 0), (100, 19000, 640, 0),
+    (33, 45001, 256, 0), (48, 45000, 400, 0)])
+def test_dense_product_of_many_tiles(n, rows, cols, pad, dtype):
+    print("case dense tiles", n, rows, cols, pad, dtype, flush=True)
+    _dense(n, rows, cols, pad, dtype)
+
+
+# tokens, top_k, experts, experts used, share dropped, rows, cols
+GROUPED_TILES = [
+    (50, 4, 64, 40, 0.2, 2000, 144),
+    (50, 4, 64, 40, 0.0, 2048, 16),
+    (64, 6, 256, 120, 0.1, 1027, 400),
+    (500, 2, 1024, 900, 0.1, 260, 256),
+    (300, 4, 40, 33, 0.1, 1500, 272),
+    (300, 4, 40, 4, 0.0, 1500, 128),
+    (400, 6, 24, 20, 0.2, 1300, 144),
+    (400, 6, 24, 24, 0.0, 1313, 528),
+    (700, 3, 5, 4, 0.1, 1100, 208),
+    (2600, 2, 6, 6, 0.3, 600, 640),
+    (900, 4, 12, 12, 1.0, 1024, 64),   # no slot has an expert
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,k,e,used,drop,rows,cols", GROUPED_TILES)
+def test_grouped_products_of_many_tiles(n, k, e, used, drop, rows, cols, dtype):
+    test_grouped_products(n, k, e, used, drop, rows, cols, dtype)
