@@ -9,6 +9,7 @@ missing, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -538,194 +539,63 @@ def moe_forward_ex(layer: Layer, logits, x, opts, routed_scale=1.5,
 # Rows in expert order, gradients of routing (moe_rows.h) and products in 8-bit
 # integers (moe_int8.h).  These calls check dtypes, shapes and layouts of their
 # tensors (ValueError) on top of the library's own checks; outputs that are
-# not given are allocated on the call's stream.
+# not given are allocated on the call's stream.  csrc/tensor_calls.cpp holds
+# the checks.
 # ----------------------------------------------------------------------------
 
-_ACT_TYPES = {torch.float32: MOE_ACT_F32, torch.bfloat16: MOE_ACT_BF16}
+_tensor_calls = None
 
 
-def _act_type(t, name):
-    """moe_act_type of a tensor's dtype."""
-    code = _ACT_TYPES.get(t.dtype if isinstance(t, torch.Tensor) else t)
-    if code is None:
-        raise ValueError("%s must be float32 or bfloat16" % name)
-    return code
+def _calls():
+    """The compiled half of the calls below (raises if it has not been built)."""
+    global _tensor_calls
+    if _tensor_calls is None:
+        lib()
+        path = os.path.join(os.path.dirname(_LIB_PATH), "tensor_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError("tensor_calls.so is not built (%s); run "
+                               "python -m block_quantized_expert_amd.build" % path)
+        spec = importlib.util.spec_from_file_location("tensor_calls", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.set_error(MoeError)
+        _tensor_calls = module
+    return _tensor_calls
 
 
-def _rows_arg(t, name, shape, dev):
-    """A matrix whose rows may be strided; returns its row stride."""
-    if t.dim() != 2 or t.shape != shape:
-        raise ValueError("%s must have shape %s, has %s" % (name, tuple(shape), tuple(t.shape)))
-    if t.device != dev:
-        raise ValueError("%s is on %s, expected %s" % (name, t.device, dev))
-    n, c = shape
-    if (c > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < c):
-        raise ValueError("%s: rows must be contiguous and must not overlap" % name)
-    return t.stride(0) if n > 1 else c
-
-
-def _dense_arg(t, name, dtype, numel, dev):
-    """A contiguous tensor of the dtype with numel elements."""
-    if t.dtype != dtype or t.numel() != numel or not t.is_contiguous() or t.device != dev:
-        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s"
-                         % (name, dtype, numel, dev))
-    return t
-
-
-class _on:
-    """The device and stream a call runs on: tensors made inside belong to
-    that stream.  ``handle`` is the stream for the library."""
-
-    __slots__ = ("stream", "handle", "guard")
-
-    def __init__(self, dev, stream):
-        if dev.type != "cuda":
-            raise ValueError("tensors must be on the GPU, got %s" % dev)
-        current = torch.cuda.current_stream(dev)
-        self.stream = current if stream is None else stream
-        self.handle = self.stream.cuda_stream
-        self.guard = None
-        if self.stream != current or dev.index != torch.cuda.current_device():
-            self.guard = torch.cuda.stream(self.stream)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        return self.handle
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-def _grouping_args(grouping, n_slots, dev):
-    counts, offsets, perm, inv_perm = grouping
-    n_experts = offsets.numel() - 1
-    _dense_arg(offsets, "offsets", torch.int32, n_experts + 1, dev)
-    for t, name in ((perm, "perm"), (inv_perm, "inv_perm")):
-        _dense_arg(t, name, torch.int32, max(n_slots, t.numel() if n_slots == 0 else 0), dev)
-    return n_experts, offsets.data_ptr(), perm.data_ptr(), inv_perm.data_ptr()
+def _call(name, stream, *args):
+    f = getattr(_tensor_calls or _calls(), name)
+    if stream is None:
+        return f(*args)
+    with torch.cuda.stream(stream):
+        return f(*args)
 
 
 def moe_dispatch(x, grouping, top_k, rows=None, stream=None):
     """Rows [n*top_k][hidden] in expert order; those that no slot has are 0."""
-    dev = x.device
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix")
-    n, h = x.shape
-    ty = _act_type(x, "x")
-    xs = _rows_arg(x, "x", (n, h), dev)
-    e, off, _, inv = _grouping_args(grouping, n * top_k, dev)
-    with _on(dev, stream) as st:
-        if rows is None:
-            rows = torch.empty((n * top_k, h), dtype=x.dtype, device=dev)
-        elif rows.dtype != x.dtype:
-            raise ValueError("rows must have x's dtype")
-        rs = _rows_arg(rows, "rows", (n * top_k, h), dev)
-        _check(lib().moe_dispatch(x.data_ptr(), ty, xs, n, top_k, h, e, off, inv,
-                                  rows.data_ptr(), rs, st), "moe_dispatch")
-    return rows
+    return _call("dispatch", stream, x, grouping, top_k, rows)
 
 
 def moe_dispatch_backward(drows, grouping, top_k, dx=None, stream=None):
     """dx [n][hidden]: the sum of a token's rows."""
-    dev = drows.device
-    if drows.dim() != 2 or top_k <= 0 or drows.shape[0] % top_k:
-        raise ValueError("drows must be a matrix of n*top_k rows")
-    slots, h = drows.shape
-    n = slots // top_k
-    ty = _act_type(drows, "drows")
-    rs = _rows_arg(drows, "drows", (slots, h), dev)
-    _, _, _, inv = _grouping_args(grouping, slots, dev)
-    with _on(dev, stream) as st:
-        if dx is None:
-            dx = torch.empty((n, h), dtype=drows.dtype, device=dev)
-        elif dx.dtype != drows.dtype:
-            raise ValueError("dx must have drows' dtype")
-        ds = _rows_arg(dx, "dx", (n, h), dev)
-        _check(lib().moe_dispatch_backward(drows.data_ptr(), ty, rs, n, top_k, h, inv,
-                                           dx.data_ptr(), ds, st), "moe_dispatch_backward")
-    return dx
+    return _call("dispatch_backward", stream, drows, grouping, top_k, dx)
 
 
 def moe_combine(rows, w, grouping, base=None, y=None, y_dtype=None, stream=None):
     """y [n][hidden] = base + the weighted sum of each token's rows.  y is of
     its own dtype, base's, y_dtype or rows' (the first that is given)."""
-    dev = rows.device
-    if rows.dim() != 2 or w.dim() != 2 or rows.shape[0] != w.numel():
-        raise ValueError("rows must be [n*top_k][hidden] and w [n][top_k]")
-    n, k = w.shape
-    h = rows.shape[1]
-    ty = _act_type(rows, "rows")
-    rs = _rows_arg(rows, "rows", (n * k, h), dev)
-    _dense_arg(w, "w", torch.float32, n * k, dev)
-    _, _, _, inv = _grouping_args(grouping, n * k, dev)
-    with _on(dev, stream) as st:
-        if y is None:
-            y_dtype = base.dtype if base is not None else (y_dtype or rows.dtype)
-            y = torch.empty((n, h), dtype=y_dtype, device=dev)
-        yt = _act_type(y, "y")
-        ys = _rows_arg(y, "y", (n, h), dev)
-        bs = 0
-        if base is not None:
-            if base.dtype != y.dtype:
-                raise ValueError("base must have y's dtype")
-            bs = _rows_arg(base, "base", (n, h), dev)
-        _check(lib().moe_combine(rows.data_ptr(), ty, rs, n, k, h, w.data_ptr(), inv,
-                                 None if base is None else base.data_ptr(), bs, y.data_ptr(), yt,
-                                 ys, st), "moe_combine")
-    return y
+    return _call("combine", stream, rows, w, grouping, base, y, y_dtype)
 
 
 def moe_combine_backward(dy, rows, w, grouping, drows=None, dw=None, stream=None):
     """(drows [n*top_k][hidden] of rows' dtype, dw fp32 [n][top_k])."""
-    dev = rows.device
-    if rows.dim() != 2 or w.dim() != 2 or rows.shape[0] != w.numel():
-        raise ValueError("rows must be [n*top_k][hidden] and w [n][top_k]")
-    n, k = w.shape
-    h = rows.shape[1]
-    ty, yt = _act_type(rows, "rows"), _act_type(dy, "dy")
-    rs = _rows_arg(rows, "rows", (n * k, h), dev)
-    ds = _rows_arg(dy, "dy", (n, h), dev)
-    _dense_arg(w, "w", torch.float32, n * k, dev)
-    e, off, _, inv = _grouping_args(grouping, n * k, dev)
-    with _on(dev, stream) as st:
-        if drows is None:
-            drows = torch.empty((n * k, h), dtype=rows.dtype, device=dev)
-        elif drows.dtype != rows.dtype:
-            raise ValueError("drows must have rows' dtype")
-        if dw is None:
-            dw = torch.empty((n, k), dtype=torch.float32, device=dev)
-        _dense_arg(dw, "dw", torch.float32, n * k, dev)
-        os_ = _rows_arg(drows, "drows", (n * k, h), dev)
-        _check(lib().moe_combine_backward(dy.data_ptr(), yt, ds, rows.data_ptr(), ty, rs, n, k, h,
-                                          e, w.data_ptr(), off, inv, drows.data_ptr(), os_,
-                                          dw.data_ptr(), st), "moe_combine_backward")
-    return drows, dw
+    return _call("combine_backward", stream, dy, rows, w, grouping, drows, dw)
 
 
 def moe_route_backward(logits, ids, dw, routed_scale=1.5, dlogits=None, dev_error=None,
                        stream=None):
     """dlogits fp32 [n][n_experts] of the learned router's weights."""
-    dev = logits.device
-    if logits.dim() != 2 or ids.dim() != 2 or ids.shape[0] != logits.shape[0]:
-        raise ValueError("logits must be [n][n_experts] and ids [n][top_k]")
-    n, e = logits.shape
-    k = ids.shape[1]
-    _dense_arg(logits, "logits", torch.float32, n * e, dev)
-    _dense_arg(ids, "ids", torch.int32, n * k, dev)
-    _dense_arg(dw, "dw", torch.float32, n * k, dev)
-    with _on(dev, stream) as st:
-        if dlogits is None:
-            dlogits = torch.empty((n, e), dtype=torch.float32, device=dev)
-        _dense_arg(dlogits, "dlogits", torch.float32, n * e, dev)
-        if dev_error is not None:
-            _dense_arg(dev_error, "dev_error", torch.int32, 1, dev)
-        _check(lib().moe_route_backward(logits.data_ptr(), ids.data_ptr(), dw.data_ptr(), n, e, k,
-                                        routed_scale, dlogits.data_ptr(),
-                                        None if dev_error is None else dev_error.data_ptr(), st),
-               "moe_route_backward")
-    return dlogits
+    return _call("route_backward", stream, logits, ids, dw, routed_scale, dlogits, dev_error)
 
 
 class Int8Weight:
@@ -738,11 +608,14 @@ class Int8Weight:
             q, scale = q.unsqueeze(0), scale.unsqueeze(0)
         if q.dim() != 3 or q.dtype != torch.int8 or not q.is_contiguous():
             raise ValueError("q must be a contiguous int8 tensor of two or three dimensions")
-        _dense_arg(scale, "scale", torch.float32, q.shape[0] * q.shape[1], q.device)
+        if (scale.dtype != torch.float32 or scale.shape != q.shape[:2] or
+                not scale.is_contiguous() or scale.device != q.device):
+            raise ValueError("scale must be a contiguous float32 tensor of shape %s on %s"
+                             % (tuple(q.shape[:2]), q.device))
         self.q, self.scale = q, scale
         self.c = MoeInt8Weight(q.shape[0], q.shape[1], q.shape[2], q.data_ptr(),
                                scale.data_ptr())
-        self.ref = ctypes.byref(self.c)
+        self.address = ctypes.addressof(self.c)
 
     @property
     def rows(self):
@@ -751,47 +624,7 @@ class Int8Weight:
 
 def moe_quantize_int8(x, q=None, scale=None, stream=None):
     """(q int8 [n][cols], scale fp32 [n]) with x ~ q * scale."""
-    dev = x.device
-    if x.dim() != 2:
-        raise ValueError("x must be a matrix")
-    n, c = x.shape
-    ty = _act_type(x, "x")
-    xs = _rows_arg(x, "x", (n, c), dev)
-    with _on(dev, stream) as st:
-        if q is None:
-            q = torch.empty((n, c), dtype=torch.int8, device=dev)
-        if scale is None:
-            scale = torch.empty(n, dtype=torch.float32, device=dev)
-        _dense_arg(q, "q", torch.int8, n * c, dev)
-        _dense_arg(scale, "scale", torch.float32, n, dev)
-        _check(lib().moe_quantize_int8(x.data_ptr(), ty, xs, n, c, q.data_ptr(),
-                                       scale.data_ptr(), st), "moe_quantize_int8")
-    return q, scale
-
-
-def _int8_call(name, weights, q, scale, grouping, top_k, out_dtype, out, stream):
-    w = weights[0]
-    dev = q.device
-    if q.dim() != 2 or q.shape[1] != w.c.cols:
-        raise ValueError("q must be [rows][%d]" % w.c.cols)
-    _dense_arg(q, "q", torch.int8, q.numel(), dev)
-    _dense_arg(scale, "scale", torch.float32, q.shape[0], dev)
-    if w.q.device != dev:
-        raise ValueError("the weights are on %s, q is on %s" % (w.q.device, dev))
-    n = q.shape[0] * (top_k or 1)
-    off = perm = None
-    if grouping is not None:
-        e, off, perm, _ = _grouping_args(grouping, n, dev)
-        if e != w.c.n_experts:
-            raise ValueError("the grouping has %d experts, the weights %d" % (e, w.c.n_experts))
-    with _on(dev, stream) as st:
-        if out is None:
-            out = torch.empty((n, w.c.rows), dtype=out_dtype, device=dev)
-        ot = _act_type(out, "out")
-        os_ = _rows_arg(out, "out", (n, w.c.rows), dev)
-        _check(getattr(lib(), name)(*[v.ref for v in weights], q.data_ptr(), scale.data_ptr(), n,
-                                    off, perm, top_k, out.data_ptr(), ot, os_, st), name)
-    return out
+    return _call("quantize_int8", stream, x, q, scale)
 
 
 def moe_product_int8(weight, q, scale, grouping=None, top_k=0, out_dtype=torch.bfloat16, out=None,
@@ -799,12 +632,12 @@ def moe_product_int8(weight, q, scale, grouping=None, top_k=0, out_dtype=torch.b
     """out [slots][rows]: q (int8 [n][cols], a scale a row) times the weight's
     rows.  With a grouping, rows of q in expert order (top_k 0) or tokens
     (top_k > 0: every slot's token is gathered)."""
-    return _int8_call("moe_product_int8", (weight,), q, scale, grouping, top_k, out_dtype, out,
-                      stream)
+    return _call("product_int8", stream, weight.address, weight.q, 0, None, q, scale, grouping,
+                 top_k, out_dtype, out)
 
 
 def moe_swiglu_int8(gate, up, q, scale, grouping=None, top_k=0, out_dtype=torch.bfloat16,
                     out=None, stream=None):
     """SwiGLU of the gate and up products; arguments as moe_product_int8."""
-    return _int8_call("moe_swiglu_int8", (gate, up), q, scale, grouping, top_k, out_dtype, out,
-                      stream)
+    return _call("product_int8", stream, gate.address, gate.q, up.address, up.q, q, scale,
+                 grouping, top_k, out_dtype, out)

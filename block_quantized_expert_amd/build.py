@@ -14,6 +14,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "lib", "libmoe.so")
+CALLS = os.path.join(PKG, "lib", "tensor_calls.so")
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 ARCH = "gfx950"
@@ -39,8 +40,25 @@ def _run(cmd):
     return "\n".join(lines)
 
 
+def _torch_flags():
+    import sysconfig
+
+    from torch.utils import cpp_extension
+
+    return ["-DUSE_ROCM=1", "-fvisibility=hidden"] + [
+        "-isystem" + p for p in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]]
+
+
+def _torch_libs():
+    from torch.utils import cpp_extension
+
+    return ["-L" + p for p in cpp_extension.library_paths()] + [
+        "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libmoe.so; returns the library path."""
+    """Compile every source and link libmoe.so and the calls on tensors;
+    returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     jobs = []
@@ -50,13 +68,20 @@ def build(verbose: bool = False) -> str:
     for src in HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
         jobs.append((obj, ["g++"] + HOST_FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]))
+    calls = os.path.join(BUILD_DIR, "tensor_calls.cpp.o")
+    jobs.insert(0, (calls, ["g++"] + HOST_FLAGS + _torch_flags()
+                    + ["-c", os.path.join(CSRC, "tensor_calls.cpp"), "-o", calls]))
     workers = min(len(jobs), max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(workers) as ex:
         logs = list(ex.map(lambda j: _run(j[1]), jobs))
     tmp = LIB + ".tmp"
     logs.append(_run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH]
-                     + [o for o, _ in jobs] + ["-o", tmp]))
+                     + [o for o, _ in jobs if o != calls] + ["-o", tmp]))
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp"
+    logs.append(_run(["g++", "-shared", calls, "-o", tmp, "-L" + os.path.dirname(LIB),
+                      "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"] + _torch_libs()))
+    os.replace(tmp, CALLS)
     if verbose:
         for log in logs:
             if log:
