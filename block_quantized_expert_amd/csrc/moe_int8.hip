@@ -269,21 +269,35 @@ constexpr int kTileGroup = 4;
 constexpr int kTableSpan = MOE_MAX_EXPERTS / kWave + 1;
 constexpr int kGridTiled = 256;  // CUs
 
-// End of a step: this wavefront's copies into LDS are done but for the newest
-// N, its LDS reads are complete (the compiler may place the barrier above the
-// products), then the workgroup's barrier.  Not __syncthreads(), whose fence
-// would wait for every copy in flight.
+// This wavefront's copies into LDS are done but for the newest N and its LDS
+// reads are complete (the compiler may place the barrier above the products
+// that use them), then the workgroup's barrier.  Not __syncthreads(), whose
+// fence would wait for every copy in flight.
 template <int N>
 __device__ __forceinline__ void step_barrier() {
   __builtin_amdgcn_s_waitcnt((N & 15) | ((N >> 4) << 14) | (0x7 << 4));
   __builtin_amdgcn_s_barrier();
 }
 
+// LDS: STAGES steps of weights [CH][128] and rows [TOK][128], then kSlots
+// tiles' scales (of the CH weight rows, and of the rows eight times each, as
+// the copies place them), then the tiles in front of each expert's.  A tile's
+// scales are copied with its first step, STAGES - 1 steps ahead; the
+// wavefronts read a tile's scales before the second barrier after its last
+// step's, so a slot may be taken again by the tile n = kSlots later if
+// (n - 1) tiles have at least STAGES steps (kMinSteps each).
 template <int TOK, int CH, int STAGES>
 struct TiledLds {
   static constexpr int kStage = (TOK + CH) * 128;
-  static constexpr int kTable = STAGES * kStage;
-  static constexpr int kBytes = kTable + 4 * (MOE_MAX_EXPERTS + 2);
+  static constexpr int kScales = STAGES * kStage;
+  static constexpr int kSlot = 4 * CH + 32 * TOK;
+  static constexpr int kTableBytes = 4 * (MOE_MAX_EXPERTS + 2);
+  static constexpr int kFree = 160 * 1024 - kScales - kTableBytes;
+  static constexpr int kSlots = kFree >= (STAGES + 1) * kSlot ? STAGES + 1 : 2;
+  static constexpr int kMinSteps = (STAGES + kSlots - 2) / (kSlots - 1);
+  static constexpr int kTable = kScales + kSlots * kSlot;
+  static constexpr int kBytes = kTable + kTableBytes;
+  static_assert(kFree >= 2 * kSlot, "LDS");
 };
 
 // Large products: TOK rows x CH rows of weights (SwiGLU: gate and up of CH / 2
@@ -296,8 +310,8 @@ struct TiledLds {
 // in flight cover the latency of HBM at its full rate.  Weights are read once
 // from memory while an expert's rows fit kTileGroup tiles.
 // 4096 x 4096 x 4096: 62 us, 2.2 POP/s (a library product of the same int8
-// matrices: 67 us), bound by the matrix cores; gate and up of 4096 tokens through 256
-// experts (4.3 GB of weights): 1.23 ms, 3.5 TB/s.
+// matrices: 67 us), bound by the matrix cores; gate and up of 4096 tokens
+// through 256 experts (4.3 GB of weights): 0.93 ms, 4.7 TB/s.
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductParams p) {
   using L = TiledLds<TOK, CH, STAGES>;
@@ -324,10 +338,14 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   // tiles in front of each expert's
   if (wave == 0) {
     int off[kTableSpan + 1], sum = 0;
+    if (grouped) {
 #pragma unroll
-    for (int i = 0; i <= kTableSpan; ++i) {
-      const int e = min(lane * kTableSpan + i, n_exp);
-      off[i] = grouped ? min(max(p.offsets[e], 0), p.n_slots) : (e == 0 ? 0 : p.n_slots);
+      for (int i = 0; i <= kTableSpan; ++i) off[i] = p.offsets[min(lane * kTableSpan + i, n_exp)];
+#pragma unroll
+      for (int i = 0; i <= kTableSpan; ++i) off[i] = min(max(off[i], 0), p.n_slots);
+    } else {
+#pragma unroll
+      for (int i = 0; i <= kTableSpan; ++i) off[i] = lane + i == 0 ? 0 : p.n_slots;
     }
 #pragma unroll
     for (int i = 0; i < kTableSpan; ++i) sum += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
@@ -392,27 +410,40 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   const char* wsrc[kW];
   const char* xsrc[kX];
   const int chunk_even = (lane % 8) ^ (lane / 16);  // rows 8j + lane / 8 of even j
-  int load_step = 0;
+  int load_step = 0, load_slot = 0;
   auto x_copy = [&](int i) { return (wave * kX + i) % (TOK / 8); };
+  // LDS row r of the weights: its matrix and channel
+  auto weight_row = [&](int r, int j0, int& ch) {
+    if (!SWIGLU) {
+      ch = min(j0 + r, p.rows - 1);
+      return 0;
+    }
+    const int blk = r / 16, b = blk % CB;
+    ch = min(j0 + (blk / CB * (CB / 2) + b % (CB / 2)) * 16 + r % 16, p.rows - 1);
+    return b < CB / 2 ? 0 : 1;
+  };
   auto open = [&]() {
     int expert, row0, m, j0;
     find(load_item, expert, row0, m, j0);
+    char* const slot = smem + L::kScales + load_slot * L::kSlot;
+    load_slot = load_slot + 1 == L::kSlots ? 0 : load_slot + 1;
+    if (wave < CH / kWave) {
+      int ch;
+      const float* w = p.w_scale[0];
+      if (weight_row(wave * kWave + lane, j0, ch) != 0) w = p.w_scale[1];
+      __builtin_amdgcn_global_load_lds(
+          w + (int64_t)expert * p.rows + ch,
+          (__attribute__((address_space(3))) void*)(slot + 4 * kWave * wave), 4, 0, 0);
+    }
 #pragma unroll
     for (int i = 0; i < kW; ++i) {
       const int j = wave * kW + i;
-      const int r = 8 * j + lane / 8;
       const int chunk = chunk_even ^ (4 * (j & 1));
       int ch;
       const int8_t* w = p.w[0];
-      if (SWIGLU) {
-        const int blk = r / 16, c = blk / CB, b = blk % CB;
-        w = b < CB / 2 ? p.w[0] : p.w[1];
-        ch = j0 + (c * (CB / 2) + b % (CB / 2)) * 16 + r % 16;
-      } else {
-        ch = j0 + r;
-      }
-      wsrc[i] = reinterpret_cast<const char*>(w) +
-                ((int64_t)expert * p.rows + min(ch, p.rows - 1)) * p.cols + 16 * chunk;
+      if (weight_row(8 * j + lane / 8, j0, ch) != 0) w = p.w[1];
+      wsrc[i] = reinterpret_cast<const char*>(w) + ((int64_t)expert * p.rows + ch) * p.cols +
+                16 * chunk;
     }
 #pragma unroll
     for (int i = 0; i < kX; ++i) {
@@ -431,25 +462,26 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         row = f >= 0 && f < p.n_slots ? f / p.top_k : 0;
       }
       xsrc[i] = reinterpret_cast<const char*>(p.q) + row * p.cols + 16 * chunk;
+      __builtin_amdgcn_global_load_lds(
+          p.scale + row,
+          (__attribute__((address_space(3))) void*)(slot + 4 * CH + 256 * j), 4, 0, 0);
     }
   };
-  // copies the next step into buffer b
-  auto issue = [&](int b) {
-    if (load_step == 0) open();
-    char* const buf = smem + b * L::kStage;
-    auto copy = [&](const char*& src, int lds_row, int j) {
-      const char* s = src;
-      if (load_step == tail &&
-          load_step * 128 + 16 * (chunk_even ^ (4 * (j & 1))) >= p.cols)
-        s = reinterpret_cast<const char*>(&kZeroChunk);
-      __builtin_amdgcn_global_load_lds(
-          s, (__attribute__((address_space(3))) void*)(buf + lds_row * 128), 16, 0, 0);
-      src += 128;
-    };
-#pragma unroll
-    for (int i = 0; i < kW; ++i) copy(wsrc[i], 8 * (wave * kW + i), wave * kW + i);
-#pragma unroll
-    for (int i = 0; i < kX; ++i) copy(xsrc[i], CH + 8 * x_copy(i), x_copy(i));
+  // copy i of the next step into buffer b, and the step's end
+  auto copy = [&](int i, int b) {
+    const bool w = i < kW;
+    const int j = w ? wave * kW + i : x_copy(i - kW);
+    const char*& src = w ? wsrc[w ? i : 0] : xsrc[w ? 0 : i - kW];
+    const char* s = src;
+    if (load_step == tail && load_step * 128 + 16 * (chunk_even ^ (4 * (j & 1))) >= p.cols)
+      s = reinterpret_cast<const char*>(&kZeroChunk);
+    __builtin_amdgcn_global_load_lds(
+        s,
+        (__attribute__((address_space(3))) void*)(smem + b * L::kStage + ((w ? 0 : CH) + 8 * j) * 128),
+        16, 0, 0);
+    src += 128;
+  };
+  auto copied = [&]() {
     if (++load_step == ksteps) {
       load_step = 0;
       load_item += per;
@@ -459,7 +491,10 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   int into = 0, from = 0, ahead = 0;
   for (int i = 0; i < STAGES - 1; ++i)
     if (load_item < end) {
-      issue(into);
+      if (load_step == 0) open();
+#pragma unroll
+      for (int c = 0; c < kW + kX; ++c) copy(c, into);
+      copied();
       into = into + 1 == STAGES ? 0 : into + 1;
       ++ahead;
     }
@@ -467,6 +502,39 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   const int swz = 16 * (g ^ (r16 / 2));
   const int woff = (wc * CB * 16 + r16) * 128 + swz;
   const int xoff = (CH + wt * TB * 16 + r16) * 128 + swz;
+  // A step is 2 TB units: half a step's 64 bytes, one block of 16 rows, all
+  // blocks of weights.  Operands are read two units ahead, the first two of
+  // a step before the step in front of it ends.
+  constexpr int U = 2 * TB;
+  constexpr int kRing = TB > 1 ? 4 : 2;  // divides U
+  constexpr int kCopies = kW + kX;
+  i32x4 wv[2][CB], xv[kRing];
+  auto read_w = [&](const char* buf, int h) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      wv[h][c] = *reinterpret_cast<const i32x4*>(buf + (woff ^ (64 * h)) + c * 2048);
+  };
+  auto read_x = [&](const char* buf, int u) {
+    xv[u % kRing] = *reinterpret_cast<const i32x4*>(buf + (xoff ^ (64 * (u / TB))) + u % TB * 2048);
+  };
+  // the next step's copies have landed, and every wavefront has read this
+  // step's operands: the buffer is free
+  auto next_step = [&]() {
+    if (ahead == STAGES - 1)
+      step_barrier<(STAGES - 2) * kCopies>();
+    else
+      step_barrier<0>();
+    from = from + 1 == STAGES ? 0 : from + 1;
+    const char* const buf = smem + from * L::kStage;
+    read_w(buf, 0);
+    read_x(buf, 0);
+    read_x(buf, 1);
+  };
+  if (item < end) {
+    from = STAGES - 1;
+    next_step();
+  }
+  int slot = 0;
   for (; item < end; item += per) {
     i32x4 acc[CB][TB];
 #pragma unroll
@@ -474,73 +542,64 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
 #pragma unroll
       for (int t = 0; t < TB; ++t) acc[c][t] = i32x4{0, 0, 0, 0};
     for (int ks = 0; ks < ksteps; ++ks) {
-      // this step's copies have landed and every wavefront is past the one
-      // before, whose buffer the next copies take
-      if (ahead == STAGES - 1)
-        step_barrier<(STAGES - 2) * (kW + kX)>();
-      else
-        step_barrier<0>();
-      if (load_item < end) {
-        issue(into);
-        into = into + 1 == STAGES ? 0 : into + 1;
-      } else {
-        --ahead;
-      }
+      const bool more = load_item < end;
+      if (more && load_step == 0) open();
       const char* const buf = smem + from * L::kStage;
-      from = from + 1 == STAGES ? 0 : from + 1;
-      // operands two products' blocks ahead of their use
-      i32x4 wv[2][CB], xv[3];
-      auto read_w = [&](int h) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (u == (TB > 2 ? TB - 2 : 0)) read_w(buf, 1);
+        if (u + 2 < U && TB > 1) read_x(buf, u + 2);
+        // Copies go between the products: a copy waits at its issue while the
+        // CU has as many lines in flight as it can (all of them in front of
+        // the products, gate and up of 4096 tokens: 1226 us instead of 970).
+        // With two stages they are needed within the step, and all go early.
+        if (more) {
+          constexpr int kSpan = STAGES == 2 ? U / 2 : U - 2 > 0 ? U - 2 : 1;
+#pragma unroll
+          for (int i = 0; i < kCopies; ++i)
+            if (i * kSpan / kCopies == u) copy(i, into);
+        }
+        if (u == U - 2) {
+          if (more) {
+            copied();
+            into = into + 1 == STAGES ? 0 : into + 1;
+          } else {
+            --ahead;
+          }
+        }
+        if (TB > 1 && u == U - 2) next_step();
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int c = 0; c < CB; ++c)
-          wv[h][c] = *reinterpret_cast<const i32x4*>(buf + (woff ^ (64 * h)) + c * 2048);
-      };
-      auto read_x = [&](int u) {
-        xv[u % 3] = *reinterpret_cast<const i32x4*>(buf + (xoff ^ (64 * (u / TB))) + u % TB * 2048);
-      };
-      read_w(0);
-      read_x(0);
-      read_x(1);
-#pragma unroll
-      for (int u = 0; u < 2 * TB; ++u) {
-        if (u == (TB > 2 ? TB - 2 : 0)) read_w(1);
-        if (u + 2 < 2 * TB) read_x(u + 2);
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-          acc[c][u % TB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u / TB][c], xv[u % 3],
+          acc[c][u % TB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u / TB][c], xv[u % kRing],
                                                                  acc[c][u % TB], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
+      if (TB == 1) next_step();
     }
     // lane: channels 4g .. 4g + 3 of its blocks for token r16
     int expert, row0, m, j0;
     find(item, expert, row0, m, j0);
+    const char* const scales = smem + L::kScales + slot * L::kSlot;
+    slot = slot + 1 == L::kSlots ? 0 : slot + 1;
     constexpr int NB = SWIGLU ? CB / 2 : CB;
-    float sg[NB][4], su[NB][4];
-#pragma unroll
-    for (int c = 0; c < NB; ++c)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = min(j0 + (wc * NB + c) * 16 + 4 * g + i, p.rows - 1);
-        const int64_t s = (int64_t)expert * p.rows + j;
-        sg[c][i] = p.w_scale[0][s];
-        su[c][i] = SWIGLU ? p.w_scale[1][s] : 0.0f;
-      }
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
       const int tok = (wt * TB + t) * 16 + r16;
       if (tok >= m) continue;
-      const int64_t row = row0 + tok;
-      const float sx = p.scale[left_row(p, row)];
-      O* const out = static_cast<O*>(p.out) + row * p.out_stride;
+      const float sx = *reinterpret_cast<const float*>(scales + 4 * CH + 32 * tok);
+      O* const out = static_cast<O*>(p.out) + (row0 + (int64_t)tok) * p.out_stride;
 #pragma unroll
       for (int c = 0; c < NB; ++c) {
         const int j = j0 + (wc * NB + c) * 16 + 4 * g;
+        const f32x4* const ws =
+            reinterpret_cast<const f32x4*>(scales + 4 * ((wc * CB + c) * 16 + 4 * g));
+        const f32x4 sg = ws[0], su = SWIGLU ? ws[4 * NB] : f32x4{0, 0, 0, 0};
         O v[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           v[i] = static_cast<O>(finish<SWIGLU>(acc[c][t][i], acc[SWIGLU ? NB + c : c][t][i], sx,
-                                               sg[c][i], su[c][i]));
+                                               sg[i], su[i]));
         if (j + 4 <= p.rows) {
           __builtin_memcpy(out + j, v, sizeof(v));
         } else {
@@ -576,8 +635,13 @@ hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
   const int64_t tiles = max_tiles(p, 16);
   const int strip = SWIGLU ? 128 : 256;
   if (tiles * ((p.rows + strip - 1) / strip) >= 2 * kGridTiled) {
+    const int steps = (p.cols + 127) / 128;
+    static_assert(TiledLds<256, 256, 2>::kMinSteps == 1 && TiledLds<64, 256, 3>::kMinSteps == 1 &&
+                      TiledLds<16, 256, 4>::kMinSteps == 1,
+                  "steps");
     if (mean > 160) return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, stream);
-    if (mean > 40) return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, stream);
+    if (mean > 40 && steps >= TiledLds<128, 256, 3>::kMinSteps)
+      return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, stream);
     if (mean > 12) return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, stream);
     return launch_tiled<SWIGLU, O, 16, 256, 1, 8, 4>(p, stream);
   }
