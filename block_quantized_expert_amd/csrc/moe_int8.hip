@@ -100,6 +100,7 @@ struct ProductParams {
   int top_k;
   void* out;
   int64_t out_stride;
+  int64_t max_tiles;  // of the direct kernel
 };
 
 // A tile of output rows row0 .. row0 + m - 1, all of one expert; expert -1:
@@ -194,7 +195,7 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
   const int r16 = lane % 16, g = lane / 16;
   const int j0 = blockIdx.x * 16;
   O* out = static_cast<O*>(p.out);
-  for (int64_t index = blockIdx.y;; index += gridDim.y) {
+  for (int64_t index = blockIdx.y; index < p.max_tiles; index += gridDim.y) {
     const Tile t = find_tile<16 * TB, PER>(p, index);
     if (t.m == 0) break;
     if (t.expert < 0) {
@@ -694,8 +695,8 @@ hipError_t launch_tiled(const ProductParams& p, hipStream_t stream) {
 }
 
 template <bool SWIGLU, typename O, int TB>
-void launch_direct(const ProductParams& p, hipStream_t stream) {
-  const int64_t tiles = max_tiles(p, 16 * TB);
+void launch_direct(ProductParams p, hipStream_t stream) {
+  const int64_t tiles = p.max_tiles = max_tiles(p, 16 * TB);
   const dim3 grid((p.rows + 15) / 16, (unsigned)(tiles < 32768 ? tiles : 32768));
   if (p.n_experts + 1 <= 5 * kWave)
     hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 5, TB>), grid, dim3(kThreads), 0, stream,
@@ -721,7 +722,7 @@ hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
                       TiledLds<16, 256, 4>::kMinSteps == 1,
                   "steps");
     if (mean > 160) return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, stream);
-    if (mean > 40 && steps >= TiledLds<128, 256, 3>::kMinSteps)
+    if (mean > 60 && steps >= TiledLds<128, 256, 3>::kMinSteps)
       return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, stream);
     if (mean > 12) return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, stream);
     return launch_tiled<SWIGLU, O, 16, 256, 1, 8, 4>(p, stream);
