@@ -47,7 +47,8 @@ __device__ __forceinline__ void load16(const T* p, float (&out)[16]) {
 }
 
 // One workgroup: one row; a thread takes 16 columns at a time, so that it
-// stores 16 bytes.  The row is read twice, the second time from cache.
+// stores 16 bytes.  Its first 16 stay in registers (4096 columns of a row);
+// columns past those are read again, from cache.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict__ x,
                                                             int64_t x_stride, int cols,
@@ -56,10 +57,16 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict_
   __shared__ uint32_t part[kWaves];
   const int64_t r = blockIdx.x;
   const T* row = x + r * x_stride;
+  const int c0 = threadIdx.x * 16;
   uint32_t top = 0;
-  for (int c = threadIdx.x * 16; c < cols; c += kThreads * 16) {
-    float v[16];
+  float v[16];
+  for (int c = c0 + kThreads * 16; c < cols; c += kThreads * 16) {
     load16(row + c, v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = max(top, magnitude(v[i]));
+  }
+  if (c0 < cols) {
+    load16(row + c0, v);
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = max(top, magnitude(v[i]));
   }
@@ -73,11 +80,10 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict_
   const bool finite = top < 0x7F800000u;
   if (threadIdx.x == 0) scale[r] = finite ? a / 127.0f : __uint_as_float(0x7FC00000u);
   const float inv = 127.0f / a;
-  for (int c = threadIdx.x * 16; c < cols; c += kThreads * 16) {
+  for (int c = c0; c < cols; c += kThreads * 16) {
     uint32_t o[4] = {0, 0, 0, 0};
     if (finite && top != 0) {
-      float v[16];
-      load16(row + c, v);
+      if (c != c0) load16(row + c, v);
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         o[i / 4] |= (uint32_t)(quantized(v[i], a, inv) & 0xFF) << (8 * (i % 4));
@@ -304,6 +310,9 @@ int64_t max_tiles(const ProductParams& p, int tm) {
 // ------------------------------------------------------------- tiled products
 
 typedef __attribute__((address_space(4))) const int32_t* scalar_i32;
+
+// Sixteen bytes of an output row, which starts at any multiple of its element.
+typedef uint32_t OutVec __attribute__((ext_vector_type(4), aligned(2)));
 
 // Sixteen bytes that a copy past the end of a row reads instead.
 __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
@@ -645,7 +654,10 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
       constexpr int B = sizeof(O) == 2 && NB % 2 == 0 ? 2 : 1;
 #pragma unroll
       for (int c = 0; c < NB; c += B) {
-        O v[4 * B];
+        struct {
+          O v[4 * B];
+        } o;
+        auto& v = o.v;
 #pragma unroll
         for (int b = 0; b < B; ++b) {
           const f32x4* const ws =
@@ -671,7 +683,13 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         }
         if (tok >= m) continue;
         if (j + 4 * B <= p.rows) {
-          __builtin_memcpy(out + j, v, sizeof(v));
+          // past the caches, which the weights go through (down of 4096
+          // tokens 533 -> 524 us; 32 bytes and less of a line lose by it)
+          if constexpr (B == 2)
+            __builtin_nontemporal_store(__builtin_bit_cast(OutVec, o),
+                                        reinterpret_cast<OutVec*>(out + j));
+          else
+            __builtin_memcpy(out + j, v, sizeof(v));
         } else {
 #pragma unroll
           for (int i = 0; i < 4 * B; ++i)

@@ -269,23 +269,30 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     s = sqrt(fmax(l, 0.0) + log1p(e));
     slope = l < -40.0 ? 0.5 * exp(0.5 * l) : (l >= 0.0 ? 1.0 : e) / (1.0 + e) / (2.0 * s);
   }
+  // lane j's values reach every lane by way of scalar registers
+  auto of_lane = [](double v, int j) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_readlane((uint32_t)u, j);
+    const uint32_t hi = __builtin_amdgcn_readlane((uint32_t)(u >> 32), j);
+    return __builtin_bit_cast(double, (uint64_t)hi << 32 | lo);
+  };
   double total = 0.0, pull = 0.0;
   for (int j = 0; j < top_k; ++j) {
-    const double sj = __shfl(s, j), dj = __shfl(d, j);
+    const double sj = of_lane(s, j), dj = of_lane(d, j);
     total += sj;
     if (sj != 0.0) pull += sj * (d - dj);
   }
   const float g = (float)(routed_scale / total * (pull / total) * slope);
-  // every lane takes part in every shuffle, also past the end of the row
-  for (int c0 = 0; c0 < n_experts; c0 += kWave) {
-    const int c = c0 + lane;
-    float out = 0.0f;
+  for (int c0 = 0; c0 < n_experts; c0 += 4 * kWave) {
+    const int c = c0 + 4 * lane;
+    float out[4] = {};
     for (int j = 0; j < top_k; ++j) {
-      const int idj = __shfl(id, j);
-      const float gj = __shfl(g, j);
-      out = c == idj ? gj : out;
+      const int at = __builtin_amdgcn_readlane(id, j) - c;
+      const float gj = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(g), j));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) out[i] = at == i ? gj : out[i];
     }
-    if (c < n_experts) dlogits[t * n_experts + c] = out;
+    if (c < n_experts) store_floats<4>(dlogits + t * n_experts + c, n_experts - c, out);
   }
 }
 
