@@ -53,7 +53,7 @@ def _torch_libs():
     from torch.utils import cpp_extension
 
     return ["-L" + p for p in cpp_extension.library_paths()] + [
-        "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_python"]
+        "-lc10", "-lc10_hip", "-ltorch_cpu", "-ltorch_hip", "-ltorch_python"]
 
 
 def build(verbose: bool = False) -> str:

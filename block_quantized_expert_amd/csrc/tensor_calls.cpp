@@ -5,7 +5,8 @@
 // binding.py holds the signatures and the documentation.
 #include <Python.h>
 
-#include <ATen/ops/empty.h>
+#include <ATen/core/Tensor.h>
+#include <ATen/hip/EmptyTensor.h>
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 #include <torch/csrc/Dtype.h>
@@ -117,8 +118,9 @@ struct On {
       : guard(dev.index()), stream(c10::hip::getCurrentHIPStream(dev.index()).stream()) {}
 };
 
+// From torch's caching allocator, on the current stream, past the dispatcher.
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, c10::Device dev) {
-  return at::empty(shape, at::TensorOptions().dtype(type).device(dev));
+  return at::Tensor(at::detail::empty_cuda(shape, type, dev, std::nullopt));
 }
 
 // The given output, of the dtype, or a new one.
