@@ -187,34 +187,37 @@ __device__ __forceinline__ O finish(int g, int u, float sx, float sg, float su) 
   return static_cast<O>(a / (1.0f + expf(-a)) * b);
 }
 
-// Small products: 16 TB rows x 16 channels a workgroup, the reduction dealt
-// to the wavefronts in turns of 128 inputs, operands straight from memory
+// Small products: 16 TB rows x 16 CB channels a workgroup (SwiGLU: CB 1, gate
+// and up), the reduction dealt to the wavefronts in turns of 128 inputs, operands straight from memory
 // into the matrix instruction, partial sums joined in LDS.  Nothing is shared
 // that a few rows could not load again, so the only waits are for memory:
 // each wavefront has 4 turns' loads (16 KiB with SwiGLU) in flight.
-template <bool SWIGLU, typename O, int PER, int TB>
+template <bool SWIGLU, typename O, int PER, int TB, int CB>
 __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams p) {
-  constexpr int M = SWIGLU ? 2 : 1;
-  constexpr int kTurns = 4;
+  static_assert(!SWIGLU || CB == 1, "blocks");
+  constexpr int M = SWIGLU ? 2 : CB;  // blocks of 16 weight rows
+  constexpr int kTurns = TB * CB > 2 ? 2 : 4;
   __shared__ i32x4 part[kWaves][M][TB][kWave];
   const int lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
   const int r16 = lane % 16, g = lane / 16;
-  const int j0 = blockIdx.x * 16;
+  const int j0 = blockIdx.x * 16 * CB;
   O* out = static_cast<O*>(p.out);
   for (int64_t index = blockIdx.y; index < p.max_tiles; index += gridDim.y) {
     const Tile t = find_tile<16 * TB, PER>(p, index);
     if (t.m == 0) break;
     if (t.expert < 0) {
-      const int j = j0 + threadIdx.x % 16;
-      for (int row = threadIdx.x / 16; row < t.m; row += kThreads / 16)
+      const int j = j0 + threadIdx.x % (16 * CB);
+      for (int row = threadIdx.x / (16 * CB); row < t.m; row += kThreads / (16 * CB))
         if (j < p.rows) out[(t.row0 + row) * p.out_stride + j] = static_cast<O>(0.0f);
       continue;
     }
     // rows and channels past the tile's end read its last one; their sums go nowhere
-    const int64_t ch = (int64_t)t.expert * p.rows + min(j0 + r16, p.rows - 1);
+    const int64_t ch0 = (int64_t)t.expert * p.rows;
     const int8_t* w[M];
 #pragma unroll
-    for (int i = 0; i < M; ++i) w[i] = p.w[i] + ch * p.cols + 16 * g;
+    for (int i = 0; i < M; ++i)
+      w[i] = p.w[SWIGLU ? i : 0] +
+             (ch0 + min(j0 + (SWIGLU ? 0 : 16 * i) + r16, p.rows - 1)) * p.cols + 16 * g;
     const int8_t* x[TB];
     int64_t lrow[TB];
 #pragma unroll
@@ -223,7 +226,7 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
       x[b] = p.q + lrow[b] * p.cols + 16 * g;
     }
     // the scales of what this wavefront finishes: block `wave` of the rows,
-    // lane: channels j0 + 4g .. +3 of row r16
+    // lane: channels 4g .. +3 of row r16 in each block
     float sx = 0.0f, sw[M][4] = {};
     if (wave < TB) {
 #pragma unroll
@@ -233,7 +236,8 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
       for (int i = 0; i < M; ++i)
 #pragma unroll
         for (int c = 0; c < 4; ++c)
-          sw[i][c] = p.w_scale[i][(int64_t)t.expert * p.rows + min(j0 + 4 * g + c, p.rows - 1)];
+          sw[i][c] = p.w_scale[SWIGLU ? i : 0]
+                              [ch0 + min(j0 + (SWIGLU ? 0 : 16 * i) + 4 * g + c, p.rows - 1)];
     }
     i32x4 acc[M][TB];
 #pragma unroll
@@ -288,12 +292,14 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
         for (int v = 1; v < kWaves; ++v) sum[i] += part[v][i][wave][lane];
       }
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int j = j0 + 4 * g + c;
-        if (j < p.rows)
-          out[(t.row0 + row) * p.out_stride + j] =
-              finish<SWIGLU, O>(sum[0][c], sum[M - 1][c], sx, sw[0][c], sw[M - 1][c]);
-      }
+      for (int i = 0; i < CB; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int j = j0 + 16 * i + 4 * g + c;
+          if (j < p.rows)
+            out[(t.row0 + row) * p.out_stride + j] = finish<SWIGLU, O>(
+                sum[i][c], sum[M - 1][c], sx, sw[i][c], sw[M - 1][c]);
+        }
     }
     __syncthreads();
   }
@@ -712,16 +718,16 @@ hipError_t launch_tiled(const ProductParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <bool SWIGLU, typename O, int TB>
+template <bool SWIGLU, typename O, int TB, int CB>
 void launch_direct(ProductParams p, hipStream_t stream) {
   const int64_t tiles = p.max_tiles = max_tiles(p, 16 * TB);
-  const dim3 grid((p.rows + 15) / 16, (unsigned)(tiles < 32768 ? tiles : 32768));
+  const dim3 grid((p.rows + 16 * CB - 1) / (16 * CB), (unsigned)(tiles < 32768 ? tiles : 32768));
   if (p.n_experts + 1 <= 5 * kWave)
-    hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 5, TB>), grid, dim3(kThreads), 0, stream,
-                       p);
+    hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 5, TB, CB>), grid, dim3(kThreads), 0,
+                       stream, p);
   else
-    hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 17, TB>), grid, dim3(kThreads), 0, stream,
-                       p);
+    hipLaunchKernelGGL((product_direct_kernel<SWIGLU, O, 17, TB, CB>), grid, dim3(kThreads), 0,
+                       stream, p);
 }
 
 template <bool SWIGLU, typename O>
@@ -745,12 +751,16 @@ hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
     if (mean > 12) return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, stream);
     return launch_tiled<SWIGLU, O, 16, 256, 1, 8, 4>(p, stream);
   }
-  // taller tiles where there are rows for them: less of the weights read again
-  // (333 x 2064 x 1235: 15.8 -> 15.1 us with the rounding)
-  if (mean >= 24)
-    launch_direct<SWIGLU, O, 2>(p, stream);
+  // larger tiles where there are rows for them and still one a CU: less of
+  // both operands read again (333 x 2064 x 1235 with the rounding: 16 x 16
+  // 15.8 us, 32 x 16 15.2, 32 x 32 14.3)
+  constexpr int kWide = SWIGLU ? 1 : 2;
+  if (mean < 24)
+    launch_direct<SWIGLU, O, 1, 1>(p, stream);
+  else if (max_tiles(p, 32) * ((p.rows + 31) / 32) < kGridTiled)
+    launch_direct<SWIGLU, O, 2, 1>(p, stream);
   else
-    launch_direct<SWIGLU, O, 1>(p, stream);
+    launch_direct<SWIGLU, O, 2, kWide>(p, stream);
   return hipGetLastError();
 }
 
