@@ -327,7 +327,7 @@ __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 // is then read from memory once and by the others from L2.
 constexpr int kTileGroup = 4;
 constexpr int kTableSpan = MOE_MAX_EXPERTS / kWave + 1;
-constexpr int kGridTiled = 256;  // CUs
+constexpr int kCus = 256;
 
 // This wavefront's copies into LDS are done but for the newest N and its LDS
 // reads are complete (the compiler may place the barrier above the products
@@ -706,15 +706,82 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   }
 }
 
+// The kernels' forms, and what a product takes with each, in microseconds,
+// fitted to every form's times over dense and grouped products of 1 to 12000
+// rows (the form chosen is the fastest or within 4 % of it in the mean).
+// Some of them, rounding included: 4096 x 4096 x 4096: 256 x 256 tiles 76 us,
+// 128 x 256 89, 128 x 128 104, 64 x 64 167; 2000 x 2048 x 2048: 36, 28, 23, 31;
+// 500 x 4096 x 2000: 57, 42, 30, 25, direct 41; 60 x 4096 x 4096: 51, 39, 27,
+// 23, direct 15; gate and up of 2000 tokens through 256 experts of 4096 x
+// 2048: 64 x 256 769, 128 x 256 819, of 5000: 1090 at 64 rows, 958 at 128,
+// 1187 at 256.
+enum Form { k256x256, k128x256, k64x256, k16x256, k128x128, k64x64, kDirect32, kDirect16 };
+struct TiledCost {
+  int rows, ch;             // tile (SwiGLU: of ch / 2 channels)
+  int per_cu;               // workgroups on a CU
+  double step, cold, tile;  // a tile's time for each step of 128 inputs, more
+                            // of it where the weights come from HBM, and once
+};
+constexpr TiledCost kTiledCost[kDirect32] = {
+    {256, 256, 1, 1.65, 0.2, 12.0}, {128, 256, 1, 1.05, 0.35, 2.0},
+    {64, 256, 1, 1.05, 0.15, 1.5},  {16, 256, 1, 0.8, 0.3, 0.8},
+    {128, 128, 1, 0.7, 0.4, 2.5},   {64, 64, 2, 0.68, 0.3, 1.1}};
+
+// Tiles of tm rows: the counts are on the device, so every expert is taken to
+// have rows and to leave nearly half a tile empty.
+double expected_tiles(const ProductParams& p, int tm) {
+  const double n = p.n_slots;
+  if (p.offsets == nullptr) return ceil(n / tm);
+  const double live = n < p.n_experts ? n : p.n_experts;
+  const double tiles = n / tm + 0.42 * live;
+  return tiles > live ? tiles : live;
+}
+
+Form choose_form(const ProductParams& p, bool swiglu) {
+  const int steps = (p.cols + 127) / 128;
+  const double live = p.n_slots < p.n_experts ? p.n_slots : p.n_experts;
+  // weights past the 256 MB memory-side cache
+  const bool cold = live * p.rows * p.cols * (swiglu ? 2 : 1) > 256e6;
+  const double mean = (double)p.n_slots / p.n_experts;
+  Form best = kDirect16;
+  double least = 0;
+  for (int wide = 0; wide < 2; ++wide) {  // bytes of both operands from L2
+    const int tm = wide ? 32 : 16, strip = wide && !swiglu ? 32 : 16;
+    const double groups = expected_tiles(p, tm) * ((p.rows + strip - 1) / strip);
+    const double bytes = groups * p.cols * ((swiglu ? 32 : strip) + (mean < tm ? mean : tm));
+    const double us = wide ? 2.1 + p.cols * 1.4e-3 + bytes * (cold ? 2.2 : 1) / 12.7e6 + groups * 3.4e-3
+                           : 1.8 + p.cols * 1.2e-3 + bytes * (cold ? 1.9 : 1) / 13.3e6 + groups * 2.2e-3;
+    if (!wide || us < least) {
+      best = wide ? kDirect32 : kDirect16;
+      least = us;
+    }
+  }
+  for (int f = 0; f < kDirect32; ++f) {
+    const TiledCost& c = kTiledCost[f];
+    if (f == k128x256 && steps < TiledLds<128, 256, 3>::kMinSteps) continue;
+    const int strip = swiglu ? c.ch / 2 : c.ch;
+    const double items = expected_tiles(p, c.rows) * ((p.rows + strip - 1) / strip);
+    const double rounds = items / (kCus * c.per_cu);
+    const double us = 4.0 + (rounds > 1 ? rounds + 0.3 : 1.0) *
+                                (steps * (c.step + (cold ? c.cold : 0)) + c.tile);
+    if (us < least) {
+      best = (Form)f;
+      least = us;
+    }
+  }
+  return best;
+}
+
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
-hipError_t launch_tiled(const ProductParams& p, hipStream_t stream) {
-  constexpr int lds = TiledLds<TOK, CH, STAGES>::kBytes;
-  static_assert(lds <= 160 * 1024, "LDS");
+hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) {
+  using L = TiledLds<TOK, CH, STAGES>;
+  static_assert(L::kBytes <= 160 * 1024, "LDS");
+  static_assert(L::kMinSteps == 1 || (TOK == 128 && CH == 256), "steps");
   constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
   static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL(kernel, dim3(kGridTiled), dim3(kWave * WT * WC), lds, stream, p);
+  hipLaunchKernelGGL(kernel, dim3(kCus * per_cu), dim3(kWave * WT * WC), L::kBytes, stream, p);
   return hipGetLastError();
 }
 
@@ -732,35 +799,17 @@ void launch_direct(ProductParams p, hipStream_t stream) {
 
 template <bool SWIGLU, typename O>
 hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
-  // The tile height follows the mean rows of an expert (the counts are on the
-  // device): rows of padding cost matrix time, a second tile of an expert
-  // another pass over its weights in L2.  Fewer tiles of 16 rows than twice
-  // the CUs: the direct kernel's more and smaller workgroups fill the chip
-  // better (one token through six experts: 25 us).
-  const int64_t mean = p.n_slots / p.n_experts;
-  const int64_t tiles = max_tiles(p, 16);
-  const int strip = SWIGLU ? 128 : 256;
-  if (tiles * ((p.rows + strip - 1) / strip) >= 2 * kGridTiled) {
-    const int steps = (p.cols + 127) / 128;
-    static_assert(TiledLds<256, 256, 2>::kMinSteps == 1 && TiledLds<64, 256, 3>::kMinSteps == 1 &&
-                      TiledLds<16, 256, 4>::kMinSteps == 1,
-                  "steps");
-    if (mean > 160) return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, stream);
-    if (mean > 60 && steps >= TiledLds<128, 256, 3>::kMinSteps)
-      return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, stream);
-    if (mean > 12) return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, stream);
-    return launch_tiled<SWIGLU, O, 16, 256, 1, 8, 4>(p, stream);
+  const Form f = choose_form(p, SWIGLU);
+  switch (f) {
+    case k256x256: return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, 1, stream);
+    case k128x256: return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, 1, stream);
+    case k64x256: return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, 1, stream);
+    case k16x256: return launch_tiled<SWIGLU, O, 16, 256, 1, 8, 4>(p, 1, stream);
+    case k128x128: return launch_tiled<SWIGLU, O, 128, 128, 2, 4, 3>(p, 1, stream);
+    case k64x64: return launch_tiled<SWIGLU, O, 64, 64, 2, 2, 3>(p, 2, stream);
+    case kDirect32: launch_direct<SWIGLU, O, 2, SWIGLU ? 1 : 2>(p, stream); break;
+    default: launch_direct<SWIGLU, O, 1, 1>(p, stream);
   }
-  // larger tiles where there are rows for them and still one a CU: less of
-  // both operands read again (333 x 2064 x 1235 with the rounding: 16 x 16
-  // 15.8 us, 32 x 16 15.2, 32 x 32 14.3)
-  constexpr int kWide = SWIGLU ? 1 : 2;
-  if (mean < 24)
-    launch_direct<SWIGLU, O, 1, 1>(p, stream);
-  else if (max_tiles(p, 32) * ((p.rows + 31) / 32) < kGridTiled)
-    launch_direct<SWIGLU, O, 2, 1>(p, stream);
-  else
-    launch_direct<SWIGLU, O, 2, kWide>(p, stream);
   return hipGetLastError();
 }
 

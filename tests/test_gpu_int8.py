@@ -315,3 +315,34 @@ GROUPED_TILES = [
 @pytest.mark.parametrize("n,k,e,used,drop,rows,cols", GROUPED_TILES)
 def test_grouped_products_of_many_tiles(n, k, e, used, drop, rows, cols, dtype):
     test_grouped_products(n, k, e, used, drop, rows, cols, dtype)
+
+
+# sizes at which the other tile shapes are chosen: 256 x 256, 128 x 256, 128 x
+# 128 and 64 x 64, plain and with SwiGLU
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,rows,cols,pad", [
+    (4339, 1870, 192, 1), (3811, 4127, 192, 0), (2335, 1697, 272, 0), (1236, 1649, 1184, 3),
+    (4170, 771, 16, 0), (4365, 227, 16, 0), (514, 3585, 272, 1), (132, 6955, 16, 0)])
+def test_dense_product_of_every_tile_shape(n, rows, cols, pad, dtype):
+    print("case dense shapes", n, rows, cols, pad, dtype, flush=True)
+    _dense(n, rows, cols, pad, dtype)
+
+
+# tokens, top_k, experts, experts used, share dropped, rows, cols
+GROUPED_FORMS = [
+    (1011, 4, 5, 5, 0.1, 450, 1696),
+    (201, 2, 8, 7, 0.2, 3972, 288),
+    (756, 6, 64, 60, 0.1, 538, 272),
+    (615, 6, 150, 140, 0.2, 187, 16),
+    (832, 2, 40, 33, 0.0, 669, 320),
+    (143, 5, 1024, 500, 0.1, 55, 16),
+    (1029, 3, 150, 120, 0.1, 162, 592),
+    (7171, 1, 1, 1, 0.1, 1047, 160),
+    (7170, 1, 1, 1, 0.05, 2276, 176),
+]
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,k,e,used,drop,rows,cols", GROUPED_FORMS)
+def test_grouped_products_of_every_tile_shape(n, k, e, used, drop, rows, cols, dtype):
+    test_grouped_products(n, k, e, used, drop, rows, cols, dtype)
