@@ -371,7 +371,9 @@ struct TiledLds {
 // from memory while an expert's rows fit kTileGroup tiles.
 // 4096 x 4096 x 4096: 62 us, 2.2 POP/s (a library product of the same int8
 // matrices: 67 us), bound by the matrix cores; gate and up of 4096 tokens
-// through 256 experts (4.3 GB of weights): 0.93 ms, 4.7 TB/s.
+// through 256 experts (4.3 GB of weights): 0.87 ms, 5.0 TB/s, bound by the
+// lines that a CU can have asked for; of 512 tokens (16 rows a tile): 0.64 ms, 6.7
+// TB/s, the memory's rate.
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductParams p) {
   using L = TiledLds<TOK, CH, STAGES>;
@@ -567,13 +569,18 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
 
   const int swz = 16 * (g ^ (r16 / 2));
   const int woff = (wc * CB * 16 + r16) * 128 + swz;
-  const int xoff = (CH + wt * TB * 16 + r16) * 128 + swz;
+  const int xoff = (CH + wt * 16 + r16) * 128 + swz;  // its blocks of rows: every WT-th
   // A step is 2 TB units: half a step's 64 bytes, one block of 16 rows, all
   // blocks of weights.  Operands are read two units ahead, the first two of
   // a step before the step in front of it ends.
   constexpr int U = 2 * TB;
   constexpr int kRing = TB > 1 ? 4 : 2;  // divides U
   constexpr int kCopies = kW + kX;
+  // Blocks past the tile's rows are left out, dealt to the WT wavefronts in
+  // turn so that they share what is left: matrix time and its power, which
+  // the clock pays for (gate and up of 4096 tokens 918 -> 882 us, of 8000
+  // 1347 -> 1271; two blocks a wavefront gain nothing, 2000 tokens 735 -> 742).
+  constexpr bool kSkip = TB > 2;
   i32x4 wv[2][CB], xv[kRing];
   auto read_w = [&](const char* buf, int h) {
 #pragma unroll
@@ -581,7 +588,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
       wv[h][c] = *reinterpret_cast<const i32x4*>(buf + (woff ^ (64 * h)) + c * 2048);
   };
   auto read_x = [&](const char* buf, int u) {
-    xv[u % kRing] = *reinterpret_cast<const i32x4*>(buf + (xoff ^ (64 * (u / TB))) + u % TB * 2048);
+    xv[u % kRing] = *reinterpret_cast<const i32x4*>(buf + (xoff ^ (64 * (u / TB))) + u % TB * WT * 2048);
   };
   // the next step's copies have landed, and every wavefront has read this
   // step's operands: the buffer is free
@@ -602,6 +609,10 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   }
   int slot = 0;
   for (; item < end; item += per) {
+    int expert, row0, m, j0;
+    bool only;
+    find(item, expert, row0, m, j0, only);
+    const int live = kSkip ? ((m + 15) / 16 - wt + WT - 1) / WT : TB;  // blocks with rows
     i32x4 acc[CB][TB];
 #pragma unroll
     for (int c = 0; c < CB; ++c)
@@ -618,9 +629,10 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         // Copies go between the products: a copy waits at its issue while the
         // CU has as many lines in flight as it can (all of them in front of
         // the products, gate and up of 4096 tokens: 1226 us instead of 970).
-        // With two stages they are needed within the step, and all go early.
+        // With two stages they are needed within the step, and all go early;
+        // so do the smaller tiles' (1024 x 4096 x 4096 34.0 -> 32.7 us).
         if (more) {
-          constexpr int kSpan = STAGES == 2 ? U / 2 : U - 2 > 0 ? U - 2 : 1;
+          constexpr int kSpan = TB > 1 ? (STAGES == 2 || CH < 256 ? U / 2 : U - 2) : 1;
 #pragma unroll
           for (int i = 0; i < kCopies; ++i)
             if (i * kSpan / kCopies == u) copy(i, into);
@@ -635,24 +647,23 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         }
         if (TB > 1 && u == U - 2) next_step();
         __builtin_amdgcn_sched_barrier(0);
+        if (!kSkip || u % TB < live) {
 #pragma unroll
-        for (int c = 0; c < CB; ++c)
-          acc[c][u % TB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u / TB][c], xv[u % kRing],
-                                                                 acc[c][u % TB], 0, 0, 0);
+          for (int c = 0; c < CB; ++c)
+            acc[c][u % TB] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[u / TB][c], xv[u % kRing],
+                                                                   acc[c][u % TB], 0, 0, 0);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       if (TB == 1) next_step();
     }
     // lane: channels 4g .. 4g + 3 of its blocks for token r16
-    int expert, row0, m, j0;
-    bool only;
-    find(item, expert, row0, m, j0, only);
     const char* const scales = smem + L::kScales + slot * L::kSlot;
     slot = slot + 1 == L::kSlots ? 0 : slot + 1;
     constexpr int NB = SWIGLU ? CB / 2 : CB;
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
-      const int tok = (wt * TB + t) * 16 + r16;
+      const int tok = (t * WT + wt) * 16 + r16;
       const float sx = *reinterpret_cast<const float*>(scales + 4 * CH + 32 * tok);
       O* const out = static_cast<O*>(p.out) + (row0 + (int64_t)tok) * p.out_stride;
       // Two blocks' bf16 values change hands between the 16-lane rows, so that
