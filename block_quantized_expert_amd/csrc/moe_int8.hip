@@ -322,9 +322,6 @@ int64_t max_tiles(const ProductParams& p, int tm) {
 
 typedef __attribute__((address_space(4))) const int32_t* scalar_i32;
 
-// Sixteen bytes of an output row, which starts at any multiple of its element.
-typedef uint32_t OutVec __attribute__((ext_vector_type(4), aligned(2)));
-
 // Sixteen bytes that a copy past the end of a row reads instead.
 __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 
@@ -612,6 +609,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     from = STAGES - 1;
     next_step();
   }
+  const bool past = grouped && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
+                    p.out_stride * sizeof(O) % 16 == 0;
   int slot = 0;
   for (; item < end; item += per) {
     int expert, row0, m, j0;
@@ -678,7 +677,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
       constexpr int B = sizeof(O) == 2 && NB % 2 == 0 ? 2 : 1;
 #pragma unroll
       for (int c = 0; c < NB; c += B) {
-        struct {
+        struct alignas(B == 2 ? 16 : sizeof(O)) {
           O v[4 * B];
         } o;
         auto& v = o.v;
@@ -707,13 +706,18 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         }
         if (tok >= m) continue;
         if (j + 4 * B <= p.rows) {
-          // past the caches, which the weights go through (down of 4096
-          // tokens 533 -> 524 us; 32 bytes and less of a line lose by it)
+          // grouped outputs past the caches, which the weights go through (down
+          // of 4096 tokens 533 -> 524 us); aligned pieces only (3647 x 6 rows
+          // of 731 channels 45.4 us, past the caches 52.7), and not a dense
+          // product's (2608 x 1344 x 3448 40.0 us, past the caches 44.2)
+          bool stored = false;
           if constexpr (B == 2)
-            __builtin_nontemporal_store(__builtin_bit_cast(OutVec, o),
-                                        reinterpret_cast<OutVec*>(out + j));
-          else
-            __builtin_memcpy(out + j, v, sizeof(v));
+            if (past) {
+              __builtin_nontemporal_store(__builtin_bit_cast(u32x4, o),
+                                          reinterpret_cast<u32x4*>(out + j));
+              stored = true;
+            }
+          if (!stored) __builtin_memcpy(out + j, v, sizeof(v));
         } else {
 #pragma unroll
           for (int i = 0; i < 4 * B; ++i)

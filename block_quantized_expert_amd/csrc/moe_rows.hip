@@ -15,6 +15,7 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMaxThreads = 512;  // of a workgroup that takes a whole token
 
 // Sixteen bytes of a row.  Rows start at any multiple of their element (an odd
 // hidden size leaves them there), which global loads and stores take as
@@ -126,7 +127,7 @@ __global__ __launch_bounds__(kThreads) void dispatch_kernel(
     T* __restrict__ rows, int64_t rows_stride) {
   constexpr int N = Vec<T>::N;
   const int64_t t = blockIdx.x;
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * N;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
   if (c >= hidden) return;
   const int m = hidden - c;
   const int64_t n_slots = (int64_t)n_tokens * K;
@@ -155,7 +156,7 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
     int64_t base_stride, Y* y, int64_t y_stride) {
   constexpr int N = Vec<T>::N;
   const int64_t t = blockIdx.x;
-  const int c = (blockIdx.y * kThreads + threadIdx.x) * N;
+  const int c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
   if (c >= hidden) return;
   const int m = hidden - c;
   int64_t row[K];
@@ -184,16 +185,16 @@ __global__ __launch_bounds__(kThreads) void combine_kernel(
 // One workgroup: one token.  dy is read once; for each slot the expert's
 // output gives the dot product and the weighted dy is stored.  The K sums are
 // reduced over the lanes by shuffles, then over the wavefronts in LDS.  Bound
-// by memory, half reads and half writes: 4096 tokens of top-6, 436 MB in 93
-// us, 4.7 TB/s (a large copy: 4.9).
-template <typename T, typename Y, int K, bool PAST, int THREADS>
-__global__ __launch_bounds__(THREADS) void combine_backward_kernel(
+// by memory, half reads and half writes: 4096 tokens of top-6, 436 MB in 87
+// us, 5.0 TB/s (a large copy: 4.9).
+template <typename T, typename Y, int K, bool PAST>
+__global__ __launch_bounds__(kMaxThreads) void combine_backward_kernel(
     const Y* __restrict__ dy, int64_t dy_stride, const T* __restrict__ rows, int64_t rows_stride,
     int n_tokens, int hidden, const int32_t* __restrict__ total,
     const float* __restrict__ topk_w, const int32_t* __restrict__ inv_perm,
     T* __restrict__ drows, int64_t drows_stride, float* __restrict__ dw) {
   constexpr int N = Vec<T>::N;
-  __shared__ float part[THREADS / kWave][K];
+  __shared__ float part[kMaxThreads / kWave][K];
   const int64_t t = blockIdx.x;
   const int64_t live = *total;
   int64_t row[K];
@@ -204,7 +205,7 @@ __global__ __launch_bounds__(THREADS) void combine_backward_kernel(
     w[i] = topk_w[t * K + i];
     dot[i] = 0.0f;
   }
-  for (int c = threadIdx.x * N; c < hidden; c += THREADS * N) {
+  for (int c = threadIdx.x * N; c < hidden; c += blockDim.x * N) {
     const int m = hidden - c;
     float d[N];
     load_floats<N>(dy + t * dy_stride + c, m, d);
@@ -238,8 +239,7 @@ __global__ __launch_bounds__(THREADS) void combine_backward_kernel(
   __syncthreads();
   if (threadIdx.x < K) {
     float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < THREADS / kWave; ++v) sum += part[v][threadIdx.x];
+    for (int v = 0; v < blockDim.x / kWave; ++v) sum += part[v][threadIdx.x];
     dw[t * K + threadIdx.x] = sum;
   }
 }
@@ -305,7 +305,15 @@ __global__ __launch_bounds__(kThreads) void route_backward_kernel(
 
 moe_status launched() { return hipGetLastError() == hipSuccess ? MOE_OK : MOE_ERR_DEVICE; }
 
-// Workgroups over a row of `hidden` elements of T, one vector a thread.
+// Threads over a row of `hidden` elements of T, a vector each: whole
+// wavefronts, so that short rows leave none idle (4096 tokens of top-6, 104
+// columns, the combine's gradient: 27.4 us with 256 threads, 11.5 with 64).
+template <typename T>
+unsigned row_threads(int hidden, int most) {
+  const int vectors = (hidden + Vec<T>::N - 1) / Vec<T>::N;
+  const int threads = (vectors + kWave - 1) / kWave * kWave;
+  return threads < most ? threads : most;
+}
 template <typename T>
 unsigned column_blocks(int hidden) {
   return (hidden + kThreads * Vec<T>::N - 1) / (kThreads * Vec<T>::N);
@@ -359,7 +367,8 @@ moe_status launch_combine(const void* rows, int type, int64_t rows_stride, int n
       with_top_k(top_k, [&](auto k) {
         with_bool(rows_aligned<T>(rows, rows_stride), [&](auto past) {
           hipLaunchKernelGGL((combine_kernel<T, Y, decltype(k)::value, decltype(past)::value>),
-                             dim3(n_tokens, column_blocks<T>(hidden)), dim3(kThreads), 0, stream,
+                             dim3(n_tokens, column_blocks<T>(hidden)),
+                             dim3(row_threads<T>(hidden, kThreads)), 0, stream,
                              static_cast<const T*>(rows), rows_stride, n_tokens, hidden, topk_w,
                              inv_perm, static_cast<const Y*>(base), base_stride,
                              static_cast<Y*>(y), y_stride);
@@ -386,8 +395,9 @@ moe_status moe_dispatch(const void* x, int type, int64_t x_stride, int n_tokens,
     using T = std::remove_pointer_t<decltype(tp)>;
     moe::with_top_k(top_k, [&](auto k) {
       hipLaunchKernelGGL((moe::dispatch_kernel<T, decltype(k)::value>),
-                         dim3(n_tokens, moe::column_blocks<T>(hidden)), dim3(moe::kThreads), 0,
-                         stream, static_cast<const T*>(x), x_stride, n_tokens, hidden,
+                         dim3(n_tokens, moe::column_blocks<T>(hidden)),
+                         dim3(moe::row_threads<T>(hidden, moe::kThreads)), 0, stream,
+                         static_cast<const T*>(x), x_stride, n_tokens, hidden,
                          offsets + n_experts, inv_perm, static_cast<T*>(rows), rows_stride);
     });
   });
@@ -433,16 +443,14 @@ moe_status moe_combine_backward(const void* dy, int y_type, int64_t dy_stride, c
       moe::with_top_k(top_k, [&](auto k) {
         moe::with_bool(moe::rows_aligned<T>(rows, rows_stride), [&](auto past) {
           // few tokens: more threads for each (512 tokens of 4096 columns 18.7
-          // -> 14.4 us; 4096 tokens 96.0 us, with 256 threads 92.8)
-          moe::with_bool(n_tokens < 2048, [&](auto few) {
-            constexpr int kBlock = decltype(few)::value ? 512 : 256;
-            hipLaunchKernelGGL((moe::combine_backward_kernel<T, Y, decltype(k)::value,
-                                                             decltype(past)::value, kBlock>),
-                               dim3(n_tokens), dim3(kBlock), 0, stream,
-                               static_cast<const Y*>(dy), dy_stride, static_cast<const T*>(rows),
-                               rows_stride, n_tokens, hidden, offsets + n_experts, topk_w,
-                               inv_perm, static_cast<T*>(drows), drows_stride, dw);
-          });
+          // -> 14.4 us; 4096 tokens 96.0 us, with 256 threads 92.8 at the time)
+          hipLaunchKernelGGL(
+              (moe::combine_backward_kernel<T, Y, decltype(k)::value, decltype(past)::value>),
+              dim3(n_tokens),
+              dim3(moe::row_threads<T>(hidden, n_tokens < 2048 ? moe::kMaxThreads : moe::kThreads)),
+              0, stream, static_cast<const Y*>(dy), dy_stride, static_cast<const T*>(rows),
+              rows_stride, n_tokens, hidden, offsets + n_experts, topk_w, inv_perm,
+              static_cast<T*>(drows), drows_stride, dw);
         });
       });
     });
