@@ -783,9 +783,11 @@ Form choose_form(const ProductParams& p, bool swiglu) {
     if (f == k128x256 && steps < TiledLds<128, 256, 3>::kMinSteps) continue;
     const int strip = swiglu ? c.ch / 2 : c.ch;
     const double items = expected_tiles(p, c.rows) * ((p.rows + strip - 1) / strip);
-    const double rounds = items / (kCus * c.per_cu);
-    const double us = 4.0 + (rounds > 1 ? rounds + 0.3 : 1.0) *
-                                (steps * (c.step + (cold ? c.cold : 0)) + c.tile);
+    // a dense product's tiles are known, its last round costs like a whole one
+    // (4061 x 3184 x 2112: 288 tiles of 128 x 256 64 us, 144 of 256 x 256 51)
+    double rounds = items / (kCus * c.per_cu);
+    rounds = p.offsets == nullptr ? ceil(rounds) : rounds > 1 ? rounds + 0.3 : 1.0;
+    const double us = 4.0 + rounds * (steps * (c.step + (cold ? c.cold : 0)) + c.tile);
     if (us < least) {
       best = (Form)f;
       least = us;

@@ -346,3 +346,11 @@ GROUPED_FORMS = [
 @pytest.mark.parametrize("n,k,e,used,drop,rows,cols", GROUPED_FORMS)
 def test_grouped_products_of_every_tile_shape(n, k, e, used, drop, rows, cols, dtype):
     test_grouped_products(n, k, e, used, drop, rows, cols, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,rows,cols,pad", [(4061, 2111, 3184, 0), (4061, 1055, 3184, 1),
+                                             (67, 5366, 16, 0), (65, 6587, 16, 3)])
+def test_dense_product_of_more_tile_shapes(n, rows, cols, pad, dtype):
+    print("case dense more shapes", n, rows, cols, pad, dtype, flush=True)
+    _dense(n, rows, cols, pad, dtype)
