@@ -354,3 +354,34 @@ def test_grouped_products_of_every_tile_shape(n, k, e, used, drop, rows, cols, d
 def test_dense_product_of_more_tile_shapes(n, rows, cols, pad, dtype):
     print("case dense more shapes", n, rows, cols, pad, dtype, flush=True)
     _dense(n, rows, cols, pad, dtype)
+
+
+def test_refusals_on_the_gpu():
+    # returned before anything is enqueued
+    x = torch.zeros(4, 64, device="cuda")
+    g = on_gpu(group(make_ids(4, 2, 8), 8))
+    with pytest.raises(B.MoeError) as e:
+        B.moe_quantize_int8(x[:, :40].contiguous())
+    assert e.value.status == B.MOE_ERR_UNSUPPORTED and "moe_quantize_int8" in str(e.value)
+    with pytest.raises(B.MoeError):
+        B.moe_route_backward(x, torch.zeros(4, 9, dtype=torch.int32, device="cuda"),
+                             torch.zeros(4, 9, device="cuda"))
+    with pytest.raises(ValueError, match="rows must have x's dtype"):
+        B.moe_dispatch(x, g, 2, rows=torch.zeros(8, 64, dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError, match="shape"):
+        B.moe_dispatch(x, g, 2, rows=torch.zeros(7, 64, device="cuda"))
+    with pytest.raises(ValueError, match="base must have"):
+        B.moe_combine(torch.zeros(8, 64, device="cuda"), torch.zeros(4, 2, device="cuda"), g,
+                      base=x, y=torch.zeros(4, 64, dtype=BF16, device="cuda"))
+    with pytest.raises(ValueError, match="expected cuda"):
+        B.moe_combine(torch.zeros(8, 64, device="cuda"), torch.zeros(4, 2, device="cuda"), g,
+                      base=x.cpu())
+    q, s = B.moe_quantize_int8(x)
+    w = B.Int8Weight(*on_gpu(int8_weight(1, 8, 32, 64)))
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        B.moe_product_int8(w, q, s, g, top_k=2, out_dtype=torch.float16)
+    with pytest.raises(B.MoeError):
+        B.moe_product_int8(w, q, s)  # several matrices, no grouping
+    with pytest.raises(B.MoeError):
+        B.moe_swiglu_int8(w, B.Int8Weight(*on_gpu(int8_weight(1, 8, 48, 64))), q, s, g, top_k=2)
+    torch.cuda.synchronize()

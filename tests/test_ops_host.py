@@ -172,3 +172,24 @@ def test_binding_refuses_host_tensors_and_wrong_layouts():
         B.moe_product_int8(w, torch.zeros(2, 32, dtype=torch.int8), torch.zeros(2))
     with pytest.raises(ValueError, match="experts"):
         B.moe_product_int8(w, torch.zeros(8, 64, dtype=torch.int8), torch.zeros(8), g)
+
+
+def test_binding_refuses_what_is_no_tensor_or_grouping():
+    x = torch.zeros(4, 64)
+    g = tuple(torch.zeros(m, dtype=torch.int32) for m in (8, 9, 8, 8))
+    with pytest.raises(TypeError, match="x must be a tensor"):
+        B.moe_dispatch([1.0], g, 2)
+    with pytest.raises(ValueError, match="grouping"):
+        B.moe_dispatch(x, g[:3], 2)
+    with pytest.raises(ValueError, match="grouping"):
+        B.moe_dispatch(x, None, 2)
+    with pytest.raises(TypeError, match="offsets must be a tensor"):
+        B.moe_dispatch(x, (g[0], None, g[2], g[3]), 2)
+    with pytest.raises(TypeError):
+        B.moe_dispatch(x, g, "2")
+    with pytest.raises(ValueError, match="out of range"):
+        B.moe_dispatch(x, g, 1 << 40)
+    with pytest.raises(ValueError, match="float32 or bfloat16"):
+        B.moe_quantize_int8(x.double())
+    with pytest.raises(ValueError, match="scale must be"):
+        B.Int8Weight(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(5))
