@@ -371,7 +371,7 @@ struct TiledLds {
 // workgroup on a CU, 256 weight rows: two or three steps of 32 KiB of weights
 // in flight cover the latency of HBM at its full rate.  Weights are read once
 // from memory while an expert's rows fit kTileGroup tiles.
-// 4096 x 4096 x 4096: 62 us, 2.2 POP/s (a library product of the same int8
+// 4096 x 4096 x 4096: 64 us, 2.1 POP/s (a library product of the same int8
 // matrices: 67 us), bound by the matrix cores; gate and up of 4096 tokens
 // through 256 experts (4.3 GB of weights): 0.87 ms, 5.0 TB/s, bound by the
 // lines that a CU can have asked for; of 512 tokens (16 rows a tile): 0.64 ms, 6.7
