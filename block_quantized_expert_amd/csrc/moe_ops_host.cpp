@@ -8,7 +8,15 @@ namespace {
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// An array of 4-byte elements (int32 or fp32).
+bool words_ok(const void* p) { return p != nullptr && aligned(p, 4); }
+
 bool type_ok(int type) { return type == MOE_ACT_F32 || type == MOE_ACT_BF16; }
+
+// A row array: aligned to its element.
+bool rows_ok(const void* p, int type) {
+  return p != nullptr && aligned(p, type == MOE_ACT_BF16 ? 2 : 4);
+}
 
 // Row strides stay far below the sizes at which an offset of rows could
 // pass 63 bits.
@@ -19,23 +27,8 @@ moe_status check_stride(int64_t stride, int width) {
   return stride > kMaxStride ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
-moe_status check_weight(const moe_int8_weight* w) {
-  if (w == nullptr) return MOE_ERR_INVALID;
-  if (w->n_experts <= 0 || w->rows <= 0 || w->cols <= 0) return MOE_ERR_INVALID;
-  if (w->n_experts > MOE_MAX_EXPERTS || w->rows > MOE_MAX_DIM || w->cols > MOE_MAX_DIM ||
-      w->cols % 16 != 0)
-    return MOE_ERR_UNSUPPORTED;
-  if (w->q == nullptr || w->scale == nullptr) return MOE_ERR_INVALID;
-  if (!aligned(w->q, 16) || !aligned(w->scale, 4)) return MOE_ERR_INVALID;
-  return MOE_OK;
-}
-
-}  // namespace
-
-bool rows_ptr_ok(const void* p, int type) {
-  return p != nullptr && aligned(p, type == MOE_ACT_BF16 ? 2 : 4);
-}
-
+// Sizes that every call on rows shares: types, counts and the strides of two
+// row arrays.
 moe_status check_rows(int type, int n_tokens, int top_k, int hidden, int64_t stride_a,
                       int64_t stride_b) {
   if (!type_ok(type)) return MOE_ERR_UNSUPPORTED;
@@ -46,6 +39,18 @@ moe_status check_rows(int type, int n_tokens, int top_k, int hidden, int64_t str
   return s != MOE_OK ? s : check_stride(stride_b, hidden);
 }
 
+moe_status check_weight(const moe_int8_weight* w) {
+  if (w == nullptr) return MOE_ERR_INVALID;
+  if (w->n_experts <= 0 || w->rows <= 0 || w->cols <= 0) return MOE_ERR_INVALID;
+  if (w->n_experts > MOE_MAX_EXPERTS || w->rows > MOE_MAX_DIM || w->cols > MOE_MAX_DIM ||
+      w->cols % 16 != 0)
+    return MOE_ERR_UNSUPPORTED;
+  if (w->q == nullptr || !aligned(w->q, 16) || !words_ok(w->scale)) return MOE_ERR_INVALID;
+  return MOE_OK;
+}
+
+}  // namespace
+
 moe_status check_dispatch(const void* x, int type, int64_t x_stride, int n_tokens, int top_k,
                           int hidden, int n_experts, const int32_t* offsets,
                           const int32_t* inv_perm, const void* rows, int64_t rows_stride) {
@@ -54,22 +59,23 @@ moe_status check_dispatch(const void* x, int type, int64_t x_stride, int n_token
   if (n_experts <= 0) return MOE_ERR_INVALID;
   if (n_experts > MOE_MAX_EXPERTS) return MOE_ERR_UNSUPPORTED;
   if (n_tokens == 0) return MOE_OK;
-  if (!rows_ptr_ok(x, type) || !rows_ptr_ok(rows, type)) return MOE_ERR_INVALID;
-  if (offsets == nullptr || inv_perm == nullptr) return MOE_ERR_INVALID;
+  if (!rows_ok(x, type) || !rows_ok(rows, type)) return MOE_ERR_INVALID;
+  if (!words_ok(offsets) || !words_ok(inv_perm)) return MOE_ERR_INVALID;
   return MOE_OK;
 }
 
 moe_status check_combine(const void* rows, int type, int64_t rows_stride, int n_tokens, int top_k,
-                         int hidden, const int32_t* inv_perm, const void* base,
-                         int64_t base_stride, const void* y, int y_type, int64_t y_stride) {
+                         int hidden, const float* topk_w, const int32_t* inv_perm,
+                         const void* base, int64_t base_stride, const void* y, int y_type,
+                         int64_t y_stride) {
   moe_status s = check_rows(type, n_tokens, top_k, hidden, rows_stride, y_stride);
   if (s != MOE_OK) return s;
   if (!type_ok(y_type)) return MOE_ERR_UNSUPPORTED;
   if (base != nullptr && (s = check_stride(base_stride, hidden)) != MOE_OK) return s;
   if (n_tokens == 0) return MOE_OK;
-  if (!rows_ptr_ok(rows, type) || !rows_ptr_ok(y, y_type)) return MOE_ERR_INVALID;
-  if (base != nullptr && !rows_ptr_ok(base, y_type)) return MOE_ERR_INVALID;
-  if (inv_perm == nullptr) return MOE_ERR_INVALID;
+  if (!rows_ok(rows, type) || !rows_ok(y, y_type)) return MOE_ERR_INVALID;
+  if (base != nullptr && !rows_ok(base, y_type)) return MOE_ERR_INVALID;
+  if (!aligned(topk_w, 4) || !words_ok(inv_perm)) return MOE_ERR_INVALID;
   return MOE_OK;
 }
 
@@ -84,19 +90,19 @@ moe_status check_combine_backward(const void* dy, int y_type, int64_t dy_stride,
   if (!type_ok(y_type)) return MOE_ERR_UNSUPPORTED;
   if ((s = check_stride(dy_stride, hidden)) != MOE_OK) return s;
   if (n_tokens == 0) return MOE_OK;
-  if (!rows_ptr_ok(dy, y_type) || topk_w == nullptr || dw == nullptr) return MOE_ERR_INVALID;
+  if (!rows_ok(dy, y_type) || !words_ok(topk_w) || !words_ok(dw)) return MOE_ERR_INVALID;
   return MOE_OK;
 }
 
 moe_status check_route_backward(const float* logits, const int32_t* ids, const float* dw,
                                 int n_tokens, int n_experts, int top_k, float routed_scale,
-                                const float* dlogits) {
+                                const float* dlogits, const int32_t* dev_error) {
   if (n_tokens < 0 || n_experts <= 0 || top_k <= 0 || top_k > n_experts) return MOE_ERR_INVALID;
   if (n_experts > MOE_MAX_EXPERTS || top_k > MOE_MAX_TOP_K || n_tokens > MOE_MAX_TOKENS)
     return MOE_ERR_UNSUPPORTED;
   if (!(routed_scale > 0.0f) || !isfinite(routed_scale)) return MOE_ERR_INVALID;
-  if (n_tokens > 0 &&
-      (logits == nullptr || ids == nullptr || dw == nullptr || dlogits == nullptr))
+  if (n_tokens > 0 && (!words_ok(logits) || !words_ok(ids) || !words_ok(dw) ||
+                       !words_ok(dlogits) || !aligned(dev_error, 4)))
     return MOE_ERR_INVALID;
   return MOE_OK;
 }
@@ -109,8 +115,8 @@ moe_status check_quantize(const void* x, int x_type, int64_t x_stride, int n_row
     return MOE_ERR_UNSUPPORTED;
   moe_status s = check_stride(x_stride, cols);
   if (s != MOE_OK || n_rows == 0) return s;
-  if (!rows_ptr_ok(x, x_type) || q == nullptr || scale == nullptr) return MOE_ERR_INVALID;
-  if (!aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_INVALID;
+  if (!rows_ok(x, x_type) || q == nullptr || !aligned(q, 16) || !words_ok(scale))
+    return MOE_ERR_INVALID;
   return MOE_OK;
 }
 
@@ -132,9 +138,9 @@ moe_status check_product(const moe_int8_weight* w, const moe_int8_weight* up, co
   if (offsets == nullptr && (w->n_experts != 1 || top_k != 0)) return MOE_ERR_INVALID;
   if (top_k > 0 && n_slots % top_k != 0) return MOE_ERR_INVALID;
   if ((s = check_stride(out_stride, w->rows)) != MOE_OK || n_slots == 0) return s;
-  if (q == nullptr || scale == nullptr || !rows_ptr_ok(out, out_type)) return MOE_ERR_INVALID;
-  if (!aligned(q, 16) || !aligned(scale, 4)) return MOE_ERR_INVALID;
-  if (top_k > 0 && perm == nullptr) return MOE_ERR_INVALID;
+  if (q == nullptr || !aligned(q, 16) || !words_ok(scale) || !rows_ok(out, out_type))
+    return MOE_ERR_INVALID;
+  if (!aligned(offsets, 4) || (top_k > 0 && !words_ok(perm))) return MOE_ERR_INVALID;
   return MOE_OK;
 }
 

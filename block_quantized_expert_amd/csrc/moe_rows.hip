@@ -407,8 +407,8 @@ moe_status moe_dispatch(const void* x, int type, int64_t x_stride, int n_tokens,
 moe_status moe_dispatch_backward(const void* drows, int type, int64_t rows_stride, int n_tokens,
                                  int top_k, int hidden, const int32_t* inv_perm, void* dx,
                                  int64_t dx_stride, hipStream_t stream) {
-  moe_status s = moe::check_combine(drows, type, rows_stride, n_tokens, top_k, hidden, inv_perm,
-                                    nullptr, 0, dx, type, dx_stride);
+  moe_status s = moe::check_combine(drows, type, rows_stride, n_tokens, top_k, hidden, nullptr,
+                                    inv_perm, nullptr, 0, dx, type, dx_stride);
   if (s != MOE_OK || n_tokens == 0) return s;
   return moe::launch_combine(drows, type, rows_stride, n_tokens, top_k, hidden, nullptr, inv_perm,
                              nullptr, 0, dx, type, dx_stride, stream);
@@ -418,7 +418,7 @@ moe_status moe_combine(const void* rows, int type, int64_t rows_stride, int n_to
                        int hidden, const float* topk_w, const int32_t* inv_perm,
                        const void* base, int64_t base_stride, void* y, int y_type,
                        int64_t y_stride, hipStream_t stream) {
-  moe_status s = moe::check_combine(rows, type, rows_stride, n_tokens, top_k, hidden, inv_perm,
+  moe_status s = moe::check_combine(rows, type, rows_stride, n_tokens, top_k, hidden, topk_w, inv_perm,
                                     base, base_stride, y, y_type, y_stride);
   if (s != MOE_OK) return s;
   if (n_tokens == 0) return MOE_OK;
@@ -462,7 +462,7 @@ moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, cons
                               int n_tokens, int n_experts, int top_k, float routed_scale,
                               float* dlogits, int32_t* dev_error, hipStream_t stream) {
   moe_status s = moe::check_route_backward(logits, topk_ids, dw, n_tokens, n_experts, top_k,
-                                           routed_scale, dlogits);
+                                           routed_scale, dlogits, dev_error);
   if (s != MOE_OK || n_tokens == 0) return s;
   constexpr int kPer = moe::kThreads / moe::kWave;
   hipLaunchKernelGGL(moe::route_backward_kernel, dim3((n_tokens + kPer - 1) / kPer),

@@ -16,8 +16,8 @@
  *   - `cols` (the length of a reduction) is a multiple of 16 up to
  *     MOE_MAX_DIM, so an int8 row is whole 16-byte words; `rows` (output
  *     channels) is any size up to MOE_MAX_DIM.  int8 arrays are 16-byte
- *     aligned and without gaps between rows; scales and outputs are aligned
- *     to their element.
+ *     aligned and without gaps between rows; scales, offsets, permutation
+ *     and outputs are aligned to their element (MOE_ERR_INVALID otherwise).
  *   - -128 is a value like any other: the int32 sum of 65536 products cannot
  *     overflow.
  */

@@ -15,7 +15,9 @@
  *     outside [0, n_tokens*top_k) is taken as -1 too.
  *   - `type` is a moe_act_type.  Strides are in elements from one row to the
  *     next and at least `hidden`; the elements of a row are contiguous and
- *     a row may start at any multiple of its element size.
+ *     a row may start at any multiple of its element size.  The other arrays
+ *     hold 4-byte elements and are aligned to them (MOE_ERR_INVALID
+ *     otherwise).
  *   - hidden is any size in 1..MOE_MAX_DIM.  Sums are taken in fp32 in slot
  *     order and rounded once to the output's type, so results do not depend
  *     on scheduling.

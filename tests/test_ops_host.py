@@ -193,3 +193,35 @@ def test_binding_refuses_what_is_no_tensor_or_grouping():
         B.moe_quantize_int8(x.double())
     with pytest.raises(ValueError, match="scale must be"):
         B.Int8Weight(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(5))
+
+
+# Arrays of 4-byte elements that are not where such elements can lie.
+@pytest.mark.parametrize("name,order,array", [
+    ("moe_dispatch", DISPATCH, "off"), ("moe_dispatch", DISPATCH, "inv"),
+    ("moe_dispatch_backward", BACK, "inv"), ("moe_combine", COMBINE, "w"),
+    ("moe_combine", COMBINE, "inv"), ("moe_combine_backward", COMBINE_BACK, "w"),
+    ("moe_combine_backward", COMBINE_BACK, "off"), ("moe_combine_backward", COMBINE_BACK, "inv"),
+    ("moe_combine_backward", COMBINE_BACK, "dw")])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_rows_refuse_misaligned_arrays(name, order, array, at):
+    misplaced = ctypes.c_void_p(P.value + at)
+    assert _call(name, order, ROWS_DEFAULTS, {array: misplaced}) == INV
+    assert _call(name, order, ROWS_DEFAULTS, {array: misplaced, "n": 0}) == OK
+
+
+@pytest.mark.parametrize("array", ["l", "ids", "dw", "dl", "err"])
+@pytest.mark.parametrize("at", [1, 2, 3])
+def test_route_backward_refuses_misaligned_arrays(array, at):
+    misplaced = ctypes.c_void_p(P.value + at)
+    assert _call("moe_route_backward", ROUTE, ROUTE_DEFAULTS, {array: misplaced}) == INV
+    assert _call("moe_route_backward", ROUTE, ROUTE_DEFAULTS, {array: misplaced, "n": 0}) == OK
+
+
+@pytest.mark.parametrize("array", ["off", "perm", "s"])
+@pytest.mark.parametrize("at", [1, 2, 3])
+@pytest.mark.parametrize("swiglu", [False, True])
+def test_product_refuses_misaligned_arrays(array, at, swiglu):
+    up = _weight() if swiglu else False
+    misplaced = ctypes.c_void_p(P.value + at)
+    assert _product(_weight(), up, {array: misplaced}) == INV
+    assert _product(_weight(), up, {array: misplaced, "n": 0}) == OK
