@@ -1,5 +1,6 @@
-"""Build libmoe.so in-tree: the HIP kernels for gfx950 plus the host-side
-C ABI, with hipcc.  ``python -m block_quantized_expert_amd.build``."""
+"""Build in-tree: libmoe.so, the HIP kernels for gfx950 plus the host-side C
+ABI, with hipcc and g++ alone; tensor_calls.so, the binding's calls on torch
+tensors, with torch's headers.  ``python -m block_quantized_expert_amd.build``."""
 
 from __future__ import annotations
 
@@ -57,8 +58,10 @@ def _torch_libs():
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libmoe.so and the calls on tensors;
-    returns the library path."""
+    """Compile every source and link libmoe.so, then the calls on tensors
+    (tensor_calls.so), which need torch's and Python's headers; returns the
+    library's path.  Without torch only the library is built; if the calls on
+    tensors do not compile, the library is in place when the error is raised."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     os.makedirs(os.path.dirname(LIB), exist_ok=True)
     jobs = []
@@ -68,20 +71,31 @@ def build(verbose: bool = False) -> str:
     for src in HOST_SOURCES:
         obj = os.path.join(BUILD_DIR, src + ".o")
         jobs.append((obj, ["g++"] + HOST_FLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]))
+    try:
+        torch_flags = _torch_flags()
+    except (ImportError, OSError) as e:
+        torch_flags = None
+        print("tensor_calls.so is not built: %s" % e, file=sys.stderr)
+        if os.path.exists(CALLS):
+            os.remove(CALLS)
     calls = os.path.join(BUILD_DIR, "tensor_calls.cpp.o")
-    jobs.insert(0, (calls, ["g++"] + HOST_FLAGS + _torch_flags()
-                    + ["-c", os.path.join(CSRC, "tensor_calls.cpp"), "-o", calls]))
-    workers = min(len(jobs), max(1, min(8, os.cpu_count() or 1)))
+    workers = min(len(jobs) + 1, max(1, min(8, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(workers) as ex:
+        compiled = None
+        if torch_flags is not None:
+            compiled = ex.submit(_run, ["g++"] + HOST_FLAGS + torch_flags + [
+                "-c", os.path.join(CSRC, "tensor_calls.cpp"), "-o", calls])
         logs = list(ex.map(lambda j: _run(j[1]), jobs))
-    tmp = LIB + ".tmp"
-    logs.append(_run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH]
-                     + [o for o, _ in jobs if o != calls] + ["-o", tmp]))
-    os.replace(tmp, LIB)
-    tmp = CALLS + ".tmp"
-    logs.append(_run(["g++", "-shared", calls, "-o", tmp, "-L" + os.path.dirname(LIB),
-                      "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"] + _torch_libs()))
-    os.replace(tmp, CALLS)
+        tmp = LIB + ".tmp"
+        logs.append(_run([HIPCC, "-shared", "-fPIC", "--offload-arch=" + ARCH]
+                         + [o for o, _ in jobs] + ["-o", tmp]))
+        os.replace(tmp, LIB)
+        if compiled is not None:
+            logs.append(compiled.result())
+            tmp = CALLS + ".tmp"
+            logs.append(_run(["g++", "-shared", calls, "-o", tmp, "-L" + os.path.dirname(LIB),
+                              "-l:libmoe.so", "-Wl,-rpath,$ORIGIN"] + _torch_libs()))
+            os.replace(tmp, CALLS)
     if verbose:
         for log in logs:
             if log:
