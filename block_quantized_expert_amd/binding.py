@@ -567,6 +567,11 @@ def _call(name, stream, *args):
     f = getattr(_tensor_calls or _calls(), name)
     if stream is None:
         return f(*args)
+    # the call takes the current stream of its tensors' device, which a stream
+    # of another device would leave as it is
+    device = next((a.device for a in args if isinstance(a, torch.Tensor)), stream.device)
+    if stream.device != device:
+        raise ValueError("stream is on %s, the tensors on %s" % (stream.device, device))
     with torch.cuda.stream(stream):
         return f(*args)
 

@@ -225,3 +225,21 @@ def test_product_refuses_misaligned_arrays(array, at, swiglu):
     misplaced = ctypes.c_void_p(P.value + at)
     assert _product(_weight(), up, {array: misplaced}) == INV
     assert _product(_weight(), up, {array: misplaced, "n": 0}) == OK
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    # streams stood in for: the check comes before anything is done with one
+    class Other:
+        device = torch.device("cuda", 1)
+
+    x = torch.zeros(4, 64)
+    g = tuple(torch.zeros(m, dtype=torch.int32) for m in (8, 9, 8, 8))
+    w = B.Int8Weight(torch.zeros(4, 64, dtype=torch.int8), torch.zeros(4))
+    q, s = torch.zeros(2, 64, dtype=torch.int8), torch.zeros(2)
+    for call in (lambda st: B.moe_dispatch(x, g, 2, stream=st),
+                 lambda st: B.moe_route_backward(x, g[0], x, stream=st),
+                 lambda st: B.moe_quantize_int8(x, stream=st),
+                 lambda st: B.moe_product_int8(w, q, s, stream=st),
+                 lambda st: B.moe_swiglu_int8(w, w, q, s, stream=st)):
+        with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cpu"):
+            call(Other())
