@@ -599,7 +599,9 @@ def moe_combine_backward(dy, rows, w, grouping, drows=None, dw=None, stream=None
 
 def moe_route_backward(logits, ids, dw, routed_scale=1.5, dlogits=None, dev_error=None,
                        stream=None):
-    """dlogits fp32 [n][n_experts] of the learned router's weights."""
+    """dlogits fp32 [n][n_experts] of the learned router's weights, from the
+    ids of a routing without tail pruning: a slot with id -1 is left out, which
+    is not the gradient of pruned weights (moe_rows.h gives dw for those)."""
     return _call("route_backward", stream, logits, ids, dw, routed_scale, dlogits, dev_error)
 
 

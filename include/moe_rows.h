@@ -75,7 +75,8 @@ moe_status moe_combine_backward(const void* dy, int y_type, int64_t dy_stride, c
 
 /*
  * Gradient of the weights of moe_route (and of moe_route_ex without tail
- * pruning: a selection by groups or with a bias has the same weights).  With
+ * pruning: a selection by groups or with a bias has the same weights; pruned
+ * weights see below).  With
  * s_i = sqrt(softplus(l_i)) of the chosen experts, S = sum_j s_j and
  * w_i = routed_scale * s_i / S,
  *   dL/dl_i = routed_scale / S^2 * sum_j s_j (dw_i - dw_j)
@@ -88,6 +89,18 @@ moe_status moe_combine_backward(const void* dy, int y_type, int64_t dy_stride, c
  *             sets MOE_DEVERR_EXPERT_ID in *dev_error (nullable).
  *   dw        fp32 [n_tokens][top_k].
  *   dlogits   out fp32 [n_tokens][n_experts], fully overwritten.
+ * Logits are finite.  Where all the chosen ones are below -700, S leaves the
+ * range of fp64 and the chosen entries are inaccurate or NaN, as the weights
+ * are.
+ *
+ * Tail pruning (keep_max, min_w) rescales: its weights are alpha * w_i on the
+ * slots that it keeps, with alpha = sqrt(A / K), A the sum of w_j^2 over all
+ * slots and K over the kept ones.  They depend on the dropped slots' logits
+ * too, and leaving those out, as the ids -1 that pruning writes would, is not
+ * their gradient.  With g the gradient by the pruned weights and
+ * G = sum_kept g_j w_j it is this call on the ids of the same routing without
+ * pruning, with
+ *   dw_i = alpha * (g_i [i kept] + G w_i (1/A - [i kept]/K)).
  */
 moe_status moe_route_backward(const float* logits, const int32_t* topk_ids, const float* dw,
                               int n_tokens, int n_experts, int top_k, float routed_scale,

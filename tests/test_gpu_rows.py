@@ -313,3 +313,40 @@ def test_route_backward_far_logits_and_left_out_slots():
     assert int(err) == B.MOE_DEVERR_EXPERT_ID
     all_out = B.moe_route_backward(l.cuda(), torch.full_like(ids, -1).cuda(), dw.cuda(), 1.5)
     assert not all_out.any()
+
+
+@pytest.mark.parametrize("keep_max,min_w", [(4, 0.0), (0, 0.24), (3, 0.26), (1, 0.0)])
+def test_gradient_of_pruned_weights_by_way_of_the_unpruned_routing(keep_max, min_w):
+    # Against central differences of the definition in 64 bits with the kept
+    # slots held (third order in a step of 1e-4: below 1e-7).  w, and so alpha, G
+    # and dw, carry a few steps of 2^-24 each: some 10 on values of up to 8,
+    # of which the router's gradient keeps less than a half: 3e-6.
+    n, e, k, scale = 8, 24, 6, 1.5
+    logits, g = normal(21, n, e), normal(22, n, k)
+    ids, w = B.moe_route(logits.cuda(), k, scale)
+    pids, pw = B.moe_route_ex(logits.cuda(), k, B.make_opts(keep_max=keep_max, min_w=min_w), scale)
+    kept = pids >= 0
+    assert torch.equal(pids[kept], ids[kept]) and 0 < int(kept.sum()) < n * k
+    w64, g64 = w.double(), g.cuda().double()
+    a = w64.square().sum(1, keepdim=True)
+    kk = (w64.square() * kept).sum(1, keepdim=True)
+    alpha = (a / kk).sqrt()
+    big_g = (g64 * w64 * kept).sum(1, keepdim=True)
+    dw = alpha * (g64 * kept + big_g * w64 * (1 / a - kept / kk))
+    dl = B.moe_route_backward(logits.cuda(), ids, dw.float(), scale).cpu().double().numpy()
+
+    ids, kept, l = ids.cpu().numpy().astype(np.int64), kept.cpu().numpy(), logits.double().numpy()
+
+    def pruned(l):
+        s = np.sqrt(np.logaddexp(0, np.take_along_axis(l, ids, 1)))
+        w = scale * s / s.sum(1, keepdims=True)
+        return w * kept * np.sqrt((w * w).sum(1, keepdims=True)
+                                  / (w * w * kept).sum(1, keepdims=True))
+
+    assert np.abs(pruned(l) - pw.cpu().double().numpy()).max() <= 8 * U32 * scale * 6 ** 0.5
+    for c in range(e):
+        up, dn = l.copy(), l.copy()
+        up[:, c] += 1e-4
+        dn[:, c] -= 1e-4
+        diff = ((pruned(up) - pruned(dn)) * g.double().numpy()).sum(1) / 2e-4
+        assert np.abs(diff - dl[:, c]).max() <= 3e-6, c
