@@ -32,7 +32,8 @@ EXPORTED = ["moe_route", "moe_route_hash", "moe_route_group", "moe_group_workspa
             "moe_stream_read", "moe_mfma_rate", "moe_mfma_rate_out_floats", "moe_route_ex", "moe_route_group_ex", "moe_ffn_forward_ex",
             "moe_forward_ex", "moe_packed_experts_bytes", "moe_pack_experts",
             "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
-            "moe_route_backward", "moe_quantize_int8", "moe_product_int8", "moe_swiglu_int8"]
+            "moe_route_backward", "moe_quantize_int8", "moe_product_int8", "moe_swiglu_int8",
+            "moe_int8_form"]
 
 WEIGHT_TYPES = {"mxfp4": MOE_W_MXFP4, "fp8_e4m3_b128": MOE_W_FP8E4M3_B128}
 
@@ -152,9 +153,11 @@ def lib() -> ctypes.CDLL:
         L.moe_quantize_int8.argtypes = [P, I, D, I, I, P, P, P]
         L.moe_product_int8.argtypes = [W, P, P, I, P, P, I, P, I, D, P]
         L.moe_swiglu_int8.argtypes = [W, W, P, P, I, P, P, I, P, I, D, P]
+        N = ctypes.POINTER(ctypes.c_int32)
+        L.moe_int8_form.argtypes = [I, I, I, I, I, I, N, N, N]
         for name in ("moe_dispatch", "moe_dispatch_backward", "moe_combine",
                      "moe_combine_backward", "moe_route_backward", "moe_quantize_int8",
-                     "moe_product_int8", "moe_swiglu_int8"):
+                     "moe_product_int8", "moe_swiglu_int8", "moe_int8_form"):
             getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -648,3 +651,12 @@ def moe_swiglu_int8(gate, up, q, scale, grouping=None, top_k=0, out_dtype=torch.
     """SwiGLU of the gate and up products; arguments as moe_product_int8."""
     return _call("product_int8", stream, gate.address, gate.q, up.address, up.q, q, scale,
                  grouping, top_k, out_dtype, out)
+
+
+def moe_int8_form(n_experts, rows, cols, n_slots, grouped, swiglu):
+    """(rows a tile, channels a tile, persistent workgroups or 0) of the kernel
+    form that an int8 product of these sizes takes (moe_probe.h)."""
+    out = [ctypes.c_int32() for _ in range(3)]
+    _check(lib().moe_int8_form(n_experts, rows, cols, n_slots, int(grouped), int(swiglu),
+                               *[ctypes.byref(v) for v in out]), "moe_int8_form")
+    return tuple(v.value for v in out)

@@ -1,7 +1,8 @@
 /*
  * moe_probe.h -- measurement helpers exported by libmoe.so: the HBM read
  * rate that a plain streaming kernel reaches on this GPU, and the issue rate
- * of the scaled matrix instruction, to report beside the published peaks.
+ * of the scaled matrix instruction, to report beside the published peaks; and
+ * the kernel form that an int8 product takes.
  * The cold scan of a buffer larger than every cache is the method of
  * "Cache-Residency Probe Results" (cism): a cold read rate is measured, not
  * taken from the vendor's figure.
@@ -56,6 +57,22 @@ moe_status moe_mfma_rate(int shape, int fmt_a, int fmt_b, int iters, float* out,
 /* The floats moe_mfma_rate writes (one per thread of its grid); 0 when the
  * device cannot be queried. */
 size_t moe_mfma_rate_out_floats(void);
+
+/*
+ * The form that moe_product_int8 (swiglu 0) or moe_swiglu_int8 (1) takes at
+ * these sizes, so that a test or a measurement can say which one it reached.
+ * Runs on the host, needs no GPU.
+ *   grouped        whether the call has offsets (without: n_experts is 1)
+ *   tile_rows      out: rows of the left operand a tile
+ *   tile_channels  out: weight rows a tile (SwiGLU: channels, each of which
+ *                  has a gate and an up row)
+ *   workgroups     out: persistent workgroups that share the tiles, 0 for the
+ *                  kernel for few rows, which has one for each tile
+ * Returns MOE_ERR_INVALID for a null pointer or sizes below 1,
+ * MOE_ERR_UNSUPPORTED for sizes past the library's limits.
+ */
+moe_status moe_int8_form(int n_experts, int rows, int cols, int n_slots, int grouped, int swiglu,
+                         int32_t* tile_rows, int32_t* tile_channels, int32_t* workgroups);
 
 #ifdef __cplusplus
 }

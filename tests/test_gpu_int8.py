@@ -356,6 +356,105 @@ def test_dense_product_of_more_tile_shapes(n, rows, cols, pad, dtype):
     _dense(n, rows, cols, pad, dtype)
 
 
+# Several tiles for every persistent workgroup, so that the rings of steps and
+# of scales run on across tiles: every tile shape, plain and with SwiGLU, with
+# reductions of one step where a shape is chosen for such, and of several
+# (test_ops_host.py checks which shapes these reach).  The 64-bit references
+# are taken on the GPU.
+SEVERAL_TILES = [
+    (65, 17021, 16, 0), (67, 33120, 16, 3), (16561, 200, 16, 0), (14482, 257, 144, 1),
+    (64, 37142, 880, 0), (16500, 272, 16, 0), (16482, 277, 144, 0), (195, 35940, 16, 0),
+    (18731, 386, 144, 0), (18287, 516, 16, 1), (36564, 258, 1424, 0), (22016, 293, 1584, 0),
+    (38470, 260, 272, 0), (36081, 273, 800, 5), (132, 38743, 816, 0), (24350, 779, 2256, 0),
+    (23415, 1695, 2192, 1),
+]
+# slots, experts, share without an expert, rows, cols
+GROUPED_SEVERAL_TILES = [
+    (240, 222, 0.0, 263, 16), (480, 283, 0.0, 278, 16), (1500, 291, 0.05, 267, 144),
+    (290, 188, 0.0, 560, 784), (4500, 145, 0.0, 275, 16), (4300, 253, 0.02, 290, 16),
+    (3900, 241, 0.0, 296, 896), (7600, 285, 0.0, 326, 16), (2400, 121, 0.0, 1040, 864),
+    (11300, 29, 0.0, 259, 144), (23600, 27, 0.01, 333, 16), (15200, 94, 0.0, 258, 2720),
+    (2700, 57, 0.0, 1264, 288), (24200, 151, 0.02, 290, 272), (20700, 154, 0.0, 274, 848),
+    (9900, 37, 0.03, 1056, 3296), (3300, 12, 0.0, 7007, 3088),
+]
+
+
+def several_tiles_offsets(slots, e, share, seed):
+    """offsets int32 [e + 1]; slots' experts are uniform, some slots have none."""
+    rng = np.random.default_rng(seed)
+    counts = np.bincount(rng.integers(0, e, slots - int(slots * share)), minlength=e)
+    return np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+
+
+def _on_gpu_product(w, q, s, offsets):
+    out = torch.zeros(q.shape[0], w.rows, dtype=torch.float64, device="cuda")
+    for e in range(w.q.shape[0]):
+        a, b = int(offsets[e]), int(offsets[e + 1])
+        if b > a:
+            acc = q[a:b].double() @ w.q[e].double().t().contiguous()
+            out[a:b] = acc * s[a:b, None].double() * w.scale[e].double()
+    return out
+
+
+def _gpu_within(got, ref, steps, what):
+    err = steps * U32 * ref.abs() * (1 + 2.0 ** -20)
+    bound = err + half_step(got.dtype) * (ref.abs() + err) + 2.0 ** -149
+    over = (got.double() - ref).abs() - bound
+    assert bool(torch.isfinite(got).all()), what
+    worst = int(over.argmax())
+    assert float(over.view(-1)[worst]) <= 0, (what, divmod(worst, ref.shape[1]))
+
+
+def _several_tiles(slots, e, rows, cols, pad, dtype, offsets, grouping, top_k=0):
+    g = torch.Generator(device="cuda").manual_seed(slots + rows)
+
+    def ints(*shape):
+        return torch.randint(-128, 128, shape, generator=g, device="cuda", dtype=torch.int8)
+
+    def uniform(lo, hi, *shape):
+        return torch.rand(*shape, generator=g, device="cuda") * (hi - lo) + lo
+
+    w, u = (B.Int8Weight(ints(e, rows, cols), uniform(0.5, 2.0, e, rows) / (74 * cols ** 0.5))
+            for _ in range(2))
+    q, s = ints(slots, cols), uniform(0.01, 0.03, slots)
+    out = strided(torch.zeros(slots, rows, dtype=dtype, device="cuda"), pad).fill_(float("nan"))
+    B.moe_product_int8(w, q, s, grouping, out=out)
+    a = _on_gpu_product(w, q, s, offsets)
+    _gpu_within(out, a, 3, "out")
+    out.fill_(float("nan"))
+    B.moe_swiglu_int8(w, u, q, s, grouping, out=out)
+    y = a / (1 + torch.exp(-a)) * _on_gpu_product(u, q, s, offsets)
+    _gpu_within(out, y, 3 * (1 + a.abs()) + 10, "swiglu")
+    assert not out[int(offsets[-1]):].any()
+    if top_k:  # every row's token gathered
+        live = int(offsets[-1])
+        tokens = (grouping[2][:live] // top_k).long()
+        qs = torch.zeros_like(q), torch.zeros_like(s)
+        q, s = q[:slots // top_k], s[:slots // top_k]
+        qs[0][:live], qs[1][:live] = q[tokens], s[tokens]
+        out.fill_(float("nan"))
+        B.moe_product_int8(w, q, s, grouping, top_k=top_k, out=out)
+        _gpu_within(out, _on_gpu_product(w, *qs, offsets), 3, "gathered")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,rows,cols,pad", SEVERAL_TILES)
+def test_dense_product_of_several_tiles_a_workgroup(n, rows, cols, pad, dtype):
+    print("case dense several", n, rows, cols, pad, dtype, flush=True)
+    _several_tiles(n, 1, rows, cols, pad, dtype, [0, n], None)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("slots,e,share,rows,cols", GROUPED_SEVERAL_TILES)
+def test_grouped_product_of_several_tiles_a_workgroup(slots, e, share, rows, cols, dtype):
+    print("case grouped several", slots, e, share, rows, cols, dtype, flush=True)
+    offsets = several_tiles_offsets(slots, e, share, seed=slots + e)
+    perm = np.random.default_rng(slots).permutation(slots).astype(np.int32)
+    perm[offsets[-1]:] = -77  # as moe_group leaves it: anything
+    grouping = on_gpu((np.diff(offsets), offsets, perm, perm))
+    _several_tiles(slots, e, rows, cols, 0, dtype, offsets, grouping, top_k=2)
+
+
 def test_refusals_on_the_gpu():
     # returned before anything is enqueued
     x = torch.zeros(4, 64, device="cuda")

@@ -243,3 +243,61 @@ def test_binding_refuses_a_stream_of_another_device():
                  lambda st: B.moe_swiglu_int8(w, w, q, s, stream=st)):
         with pytest.raises(ValueError, match="stream is on cuda:1, the tensors on cpu"):
             call(Other())
+
+
+TILE_SHAPES = [(256, 256), (128, 256), (64, 256), (16, 256), (128, 128), (64, 64)]
+
+
+@pytest.mark.parametrize("sizes,expected", [
+    ((0, 8, 16, 1, 1, 0), INV), ((1, 0, 16, 1, 1, 0), INV), ((1, 8, 0, 1, 1, 0), INV),
+    ((1, 8, 16, 0, 1, 0), INV), ((2, 8, 16, 1, 0, 0), INV), ((1025, 8, 16, 1, 1, 0), UNS),
+    ((1, 65537, 16, 1, 1, 0), UNS), ((1, 8, 24, 1, 1, 0), UNS), ((1, 8, 65552, 1, 1, 0), UNS),
+    ((1, 8, 16, (1 << 25) + 1, 1, 0), UNS)])
+def test_int8_form_refuses(sizes, expected):
+    out = [ctypes.c_int32() for _ in range(3)]
+    assert B.lib().moe_int8_form(*sizes, *[ctypes.byref(v) for v in out]) == expected
+
+
+def test_int8_form_refuses_null():
+    v = ctypes.byref(ctypes.c_int32())
+    for null in range(3):
+        out = [None if i == null else v for i in range(3)]
+        assert B.lib().moe_int8_form(1, 8, 16, 1, 1, 0, *out) == INV
+
+
+def test_int8_forms_of_few_rows_have_no_persistent_workgroups():
+    assert B.moe_int8_form(1, 4096, 4096, 1, False, False) == (16, 16, 0)
+    assert B.moe_int8_form(256, 2048, 4096, 6, True, True) == (16, 16, 0)
+
+
+def test_gpu_cases_take_every_int8_tile_shape_across_tiles():
+    """Every tile shape, plain and with SwiGLU, dense and grouped, is chosen by a
+    case of test_gpu_int8.py that gives every persistent workgroup two tiles
+    and more; where the shape is chosen for reductions of one step, one of those
+    has such a reduction."""
+    import test_gpu_int8 as G
+
+    reached, one_step = set(), set()
+
+    def look(kind, e, rows, cols, counts, slots):
+        for swiglu in (False, True):
+            r, c, workgroups = B.moe_int8_form(e, rows, cols, slots, kind == "grouped", swiglu)
+            items = sum(-(-int(n) // r) for n in counts) * -(-rows // c)
+            if workgroups and items >= 2 * workgroups:
+                key = (kind, swiglu, r, c * 2 if swiglu else c)
+                reached.add(key)
+                if cols <= 128:
+                    one_step.add(key[1:])
+
+    for n, rows, cols, _ in G.SEVERAL_TILES:
+        look("dense", 1, rows, cols, [n], n)
+    for slots, e, share, rows, cols in G.GROUPED_SEVERAL_TILES:
+        off = G.several_tiles_offsets(slots, e, share, seed=slots + e)
+        look("grouped", e, rows, cols, off[1:] - off[:-1], slots)
+    want = {(kind, swiglu, r, c) for kind in ("dense", "grouped") for swiglu in (False, True)
+            for r, c in TILE_SHAPES}
+    assert reached == want, sorted(want - reached)
+    # 256 x 256 tiles are taken for long reductions, 128 x 256 for three steps
+    # and more, 128 x 128 of SwiGLU mostly for several
+    short = {(swiglu, r, c) for swiglu in (False, True) for r, c in TILE_SHAPES[2:]}
+    assert one_step >= short - {(True, 128, 128)}, sorted(short - one_step)
