@@ -455,6 +455,32 @@ def test_grouped_product_of_several_tiles_a_workgroup(slots, e, share, rows, col
     _several_tiles(slots, e, rows, cols, 0, dtype, offsets, grouping, top_k=2)
 
 
+def test_products_on_groupings_of_moe_group_with_dropped_slots():
+    # moe_group writes perm up to the last expert's row only
+    n, k, e, rows, cols = 90, 4, 16, 48, 208
+    ids = make_ids(n, k, e, 0.3, seed=11)
+    counts, off, perm, inv = group(ids, e)
+    total = int(off[-1])
+    g = [torch.full((m,), 0x7F7F7F7F, dtype=torch.int32, device="cuda")
+         for m in (e, e + 1, n * k, n * k)]
+    grouping = B.moe_group(torch.from_numpy(ids).cuda(), e, out=tuple(g))
+    assert np.array_equal(grouping[1].cpu().numpy(), off) and 0 < total < n * k
+    (gq, gs), (uq, us) = int8_weight(1, e, rows, cols), int8_weight(2, e, rows, cols)
+    gate, up = (B.Int8Weight(*on_gpu(w)) for w in ((gq, gs), (uq, us)))
+    q, s = _left(n, cols, 3)
+    left = perm // k
+    a, b = (product_ref(*w, q, s, off, left) for w in ((gq, gs), (uq, us)))
+    out = torch.full((n * k, rows), float("nan"), dtype=F32, device="cuda")
+    B.moe_product_int8(gate, *on_gpu((q, s)), grouping, top_k=k, out=out)
+    assert_within(out, a, _bound(a, F32, 3), "product")
+    assert not out[total:].any()
+    out.fill_(float("nan"))
+    B.moe_swiglu_int8(gate, up, *on_gpu((q, s)), grouping, top_k=k, out=out)
+    y, steps = _swiglu(a, b)
+    assert_within(out, y, _bound(y, F32, steps), "swiglu")
+    assert not out[total:].any()
+
+
 def test_refusals_on_the_gpu():
     # returned before anything is enqueued
     x = torch.zeros(4, 64, device="cuda")
