@@ -54,7 +54,8 @@ moe_status moe_quantize_int8(const void* x, int x_type, int64_t x_stride, int n_
 
 /*
  * out[p][j] = scale[r] * w.scale[e][j] * sum_k q[r][k] * w.q[e][j][k],
- * rounded once to out_type.
+ * rounded once to out_type; the sum takes its two factors in fp32 in the order
+ * scale, w.scale.
  *   Dense (offsets NULL): w has one matrix, n_slots rows, r = p.
  *   Grouped: offsets (int32 [n_experts+1], moe_group's) gives the rows
  *     offsets[e] .. offsets[e+1]-1 to expert e.  With top_k == 0 the left
@@ -72,7 +73,8 @@ moe_status moe_product_int8(const moe_int8_weight* w, const int8_t* q, const flo
  * The gate and up products of the same rows with SwiGLU in their epilogue:
  * out = g / (1 + exp(-g)) * u with g, u as moe_product_int8 would give them
  * in fp32, rounded once to out_type.  gate and up have the same shape.  The
- * other arguments are moe_product_int8's.
+ * other arguments are moe_product_int8's.  Below g = -87, where exp(-g)
+ * leaves fp32, out may be 0 (the exact value is below 1.5e-36 |u|).
  */
 moe_status moe_swiglu_int8(const moe_int8_weight* gate, const moe_int8_weight* up,
                            const int8_t* q, const float* scale, int n_slots,

@@ -209,6 +209,41 @@ def test_swiglu_of_far_gates():
     assert_within(out, y, _bound(y, F32, 3 * (1 + np.abs(a)) + 10) + 1e-30, "far gates")
 
 
+FAR = [0.0, 0.5, 20, 60, 80, 86, 87, 87.5, 88, 88.5, 88.8, 89, 90, 100, 104, 127, 300, 1000]
+
+
+# rows and channels of the kernel for few rows and of tiled ones, 16-byte
+# bf16 stores among them, dense (experts 0) and grouped
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,e,rows,cols,tiled", [
+    (36, 0, 40, 64, False), (36, 3, 33, 64, False), (1024, 0, 8192, 128, True),
+    (700, 0, 6001, 512, True), (680, 4, 2048, 256, True), (4000, 1, 2048, 1024, True)])
+def test_swiglu_of_far_gates_in_every_epilogue(n, e, rows, cols, tiled, dtype):
+    # Gates around the places where exp(-g) leaves fp32 and its reciprocal the
+    # normal numbers, and far past them.  The hardware's exponential and
+    # reciprocal add 2 |g| half-steps of fp32 to the bound above; below -87 a
+    # value may be 0, where the true one is at most 87 e^-87 |u|.  Half a step
+    # of a subnormal bf16 is 2^-134, whatever its value.
+    assert (B.moe_int8_form(e or 1, rows, cols, n, e > 0, True)[2] > 0) == tiled
+    gates = np.resize(np.array(FAR + [-v for v in FAR], np.float32), n)
+    ones = np.ones((e or 1, rows, cols), np.int8)
+    uq, us = int8_weight(6, e or 1, rows, cols)
+    q = np.where(gates < 0, -1, 1).astype(np.int8)[:, None].repeat(cols, 1)
+    s = np.abs(gates) / np.float32(cols)
+    unit = np.ones((e or 1, rows), np.float32)
+    offsets = np.array([0, n]) if e == 0 else np.linspace(0, n, e + 1).astype(np.int32)
+    filler = np.arange(n, dtype=np.int32)
+    grouping = on_gpu((np.diff(offsets), offsets, filler, filler)) if e else None
+    got = B.moe_swiglu_int8(*(B.Int8Weight(*on_gpu(w)) for w in ((ones, unit), (uq, us))),
+                            *on_gpu((q, s)), grouping, out_dtype=dtype)
+    a = product_ref(ones, unit, q, s, offsets, np.arange(n))
+    u = product_ref(uq, us, q, s, offsets, np.arange(n))
+    y = a * np.exp(-np.logaddexp(0, -a)) * u
+    tol = _bound(y, dtype, 3 * (1 + np.abs(a)) + 10 + 2 * np.abs(a))
+    tol += 2.0 ** -134 if dtype == BF16 else 0
+    assert_within(got, y, tol + np.where(a < -86.9, 1.5e-36 * np.abs(u), 0), "far gates")
+
+
 def test_no_slots():
     w = B.Int8Weight(*on_gpu(int8_weight(1, 4, 32, 64)))
     g = on_gpu(group(make_ids(0, 2, 4), 4))
