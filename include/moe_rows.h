@@ -64,8 +64,10 @@ moe_status moe_combine(const void* rows, int type, int64_t rows_stride, int n_to
  *   drows[p]    = topk_w[f] * dy[f / top_k] for p = inv_perm[f], of `type`
  *   dw[t][i]    = <dy[t], rows[inv_perm[t*top_k + i]]>, fp32; 0 for a slot
  *                 without a row
- * (the gradient of base is dy).  The dot product is summed in fp32 in a
- * fixed order.
+ * (the gradient of base is dy).  The dot product is summed in fp32 in an order
+ * that n_tokens, hidden and the types fix, so a call repeats bit for bit, but
+ * dw of the same token may differ in its last bits between batches of fewer
+ * than 2048 tokens and larger ones.
  */
 moe_status moe_combine_backward(const void* dy, int y_type, int64_t dy_stride, const void* rows,
                                 int type, int64_t rows_stride, int n_tokens, int top_k,

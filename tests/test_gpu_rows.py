@@ -350,3 +350,35 @@ def test_gradient_of_pruned_weights_by_way_of_the_unpruned_routing(keep_max, min
         dn[:, c] -= 1e-4
         diff = ((pruned(up) - pruned(dn)) * g.double().numpy()).sum(1) / 2e-4
         assert np.abs(diff - dl[:, c]).max() <= 3e-6, c
+
+
+# 2048 tokens and more: 256 threads a token at most, several rounds of columns
+# for each (bf16 above 2048 columns, fp32 above 1024), aligned rows and others.
+# The references are taken in 64 bits on the GPU.
+@pytest.mark.parametrize("dtype,y_dtype", [(BF16, BF16), (BF16, F32), (F32, F32), (F32, BF16)])
+@pytest.mark.parametrize("n,k,e,h,drop,pad", [
+    (2048, 2, 16, 4096, 0.0, 0), (2049, 3, 37, 2059, 0.2, 1), (2500, 1, 8, 4104, 0.0, 0),
+    (2047, 2, 16, 4096, 0.1, 0), (4097, 6, 64, 1032, 0.1, 0), (2048, 8, 256, 5003, 0.3, 3)])
+def test_combine_backward_of_large_batches(n, k, e, h, drop, pad, dtype, y_dtype):
+    print("case combine_backward large", n, k, e, h, drop, pad, dtype, y_dtype, flush=True)
+    ids, (_, off, perm, inv), g = _case(n, k, e, drop)
+    total = int(off[-1])
+    gen = torch.Generator(device="cuda").manual_seed(n + h)
+    rows, dy, w = (torch.randn(*shape, generator=gen, device="cuda").to(t) for shape, t in
+                   (((n * k, h), dtype), ((n, h), y_dtype), ((n, k), F32)))
+    rows[total:] = float("nan")
+    rows, dy = strided(rows, pad), strided(dy, pad)
+    drows, dw = B.moe_combine_backward(dy, rows, w, g)
+    f = g[2][:total].long()
+    ref = w.view(-1)[f, None].double() * dy[f // k].double()
+    over = (drows[:total].double() - ref).abs() - ref.abs() * (U32 + half_step(dtype) * (1 + U32))
+    assert float(over.max()) <= 0
+    assert not drows[total:].any()
+    terms = dy[f // k].double() * rows[:total].double()
+    chain = 8 * -(-h // 1024) + 10  # a lane's columns, six steps over the lanes, four wavefronts
+    over = (dw.view(-1)[f].double() - terms.sum(1)).abs() - chain * U32 * terms.abs().sum(1)
+    assert float(over.max()) <= 0
+    dropped = torch.from_numpy(inv < 0).cuda()
+    assert not dw.view(-1)[dropped].any()
+    again = B.moe_combine_backward(dy, rows, w, g)
+    assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
