@@ -81,6 +81,30 @@ def test_quantize_zero_and_non_finite_rows(dtype):
     assert np.array_equal(s[1:3], np.zeros(2, np.float32)) and np.isnan(s[3:]).all()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_quantize_more_rows_than_a_launch_takes(dtype):
+    # rows go in launches of 2^22; the reference in 64 bits on the GPU
+    n, c = (1 << 22) + 5, 16
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(n, c, generator=g, device="cuda").to(dtype)
+    for r in ((1 << 22) - 1, 1 << 22, n - 1):
+        x[r] *= 100
+    x[(1 << 22) + 1] = 0
+    x[(1 << 22) + 2, 3] = float("inf")
+    q = torch.full((n, c), 77, dtype=torch.int8, device="cuda")
+    s = torch.full((n,), -1.0, device="cuda")
+    B.moe_quantize_int8(x, q=q, scale=s)
+    bad = (1 << 22) + 2
+    assert bool(s[bad].isnan()) and not q[bad].any()
+    x[bad] = 0
+    a = x.double().abs().amax(1, keepdim=True)
+    ref = torch.round(x.double() * 127 / a.clamp_min(1e-300)).to(torch.int8)
+    assert torch.equal(q, ref)
+    s[bad] = 0
+    # from 64 bits: torch takes an fp32 tensor over a number by its reciprocal
+    assert torch.equal(s, (a[:, 0] / 127).float())
+
+
 def _bound(ref, dtype, steps):
     err = steps * U32 * np.abs(ref) * (1 + 2.0 ** -20)
     return err + half_step(dtype) * (np.abs(ref) + err) + 2.0 ** -149
