@@ -544,6 +544,13 @@ def moe_forward_ex(layer: Layer, logits, x, opts, routed_scale=1.5,
 # tensors (ValueError) on top of the library's own checks; outputs that are
 # not given are allocated on the call's stream.  csrc/tensor_calls.cpp holds
 # the checks.
+#
+# Like the calls above they are not recorded by autograd: an output never
+# requires a gradient, whatever the inputs do.  examples/experts_around.py puts
+# each forward and its gradient into a torch.autograd.Function.  New outputs
+# come from torch's caching allocator past its dispatcher, so dispatch modes
+# and the filling of uninitialised memory do not see them; the kernels write
+# every element.
 # ----------------------------------------------------------------------------
 
 _tensor_calls = None
@@ -580,7 +587,8 @@ def _call(name, stream, *args):
 
 
 def moe_dispatch(x, grouping, top_k, rows=None, stream=None):
-    """Rows [n*top_k][hidden] in expert order; those that no slot has are 0."""
+    """Rows [n*top_k][hidden] in expert order; those that no slot has are 0.
+    Not recorded by autograd (gradient: moe_dispatch_backward)."""
     return _call("dispatch", stream, x, grouping, top_k, rows)
 
 
@@ -591,7 +599,8 @@ def moe_dispatch_backward(drows, grouping, top_k, dx=None, stream=None):
 
 def moe_combine(rows, w, grouping, base=None, y=None, y_dtype=None, stream=None):
     """y [n][hidden] = base + the weighted sum of each token's rows.  y is of
-    its own dtype, base's, y_dtype or rows' (the first that is given)."""
+    its own dtype, base's, y_dtype or rows' (the first that is given).  Not
+    recorded by autograd (gradients: moe_combine_backward)."""
     return _call("combine", stream, rows, w, grouping, base, y, y_dtype)
 
 

@@ -382,3 +382,13 @@ def test_combine_backward_of_large_batches(n, k, e, h, drop, pad, dtype, y_dtype
     assert not dw.view(-1)[dropped].any()
     again = B.moe_combine_backward(dy, rows, w, g)
     assert torch.equal(again[0], drows) and torch.equal(again[1], dw)
+
+
+def test_autograd_records_nothing():
+    n, k, e, h = 5, 2, 4, 24
+    _, _, g = _case(n, k, e, 0.0)
+    x, w = (normal(i, n, c).cuda().requires_grad_() for i, c in ((1, h), (2, k)))
+    rows = B.moe_dispatch(x, g, k)
+    y = B.moe_combine(rows, w, g, base=x)
+    for t in (rows, y, B.moe_dispatch_backward(rows, g, k)) + B.moe_combine_backward(y, rows, w, g):
+        assert not t.requires_grad and t.grad_fn is None
