@@ -181,6 +181,8 @@ __device__ __forceinline__ int64_t left_row(const ProductParams& p, int64_t row)
 // Scales, SwiGLU and the rounding to the output's type.  For bf16 the hardware's
 // exponential and reciprocal serve: they are off by some (|a| + 4) 2^-24,
 // next to the 2^-9 of the rounding, and take a third of the instructions.
+// Below a = -87 the sum or its reciprocal leaves the normal numbers and the
+// result may be 0 (of at most 1.5e-36 |b|), in fp32 from -88.7 on.
 template <bool SWIGLU, typename O>
 __device__ __forceinline__ O finish(int g, int u, float sx, float sg, float su) {
   const float a = (float)g * sx * sg;
@@ -370,13 +372,16 @@ struct TiledLds {
 // that goes from tile to tile never waits for a first load; LDS also turns
 // whole 128-byte lines of memory into the matrix instruction's layout.  One
 // workgroup on a CU, 256 weight rows: two or three steps of 32 KiB of weights
-// in flight cover the latency of HBM at its full rate.  Weights are read once
-// from memory while an expert's rows fit kTileGroup tiles.
-// 4096 x 4096 x 4096: 64 us, 2.1 POP/s (a library product of the same int8
-// matrices: 67 us), bound by the matrix cores; gate and up of 4096 tokens
-// through 256 experts (4.3 GB of weights): 0.87 ms, 5.0 TB/s, bound by the
-// lines that a CU can have asked for; of 512 tokens (16 rows a tile): 0.64 ms, 6.7
-// TB/s, the memory's rate.
+// in flight.  Weights are read once from memory while an expert's rows fit
+// kTileGroup tiles.
+// 4096 x 4096 x 4096: 68 us, 2.0 POP/s (three sets of matrices in turn; a
+// library's int8 product of the same ones 65.5, and both are faster on small
+// values), matrix cores busy 40 % of the time; gate and up of 4096 tokens
+// through 256 experts (4.3 GB of weights): 0.86 ms, 4.78 GB moved at 5.5 TB/s,
+// a plain streaming read's rate (5.4), matrix cores busy 25 %, address units
+// 67 %; of 512 tokens (12 rows an expert, 64-row tiles, weights past the
+// caches): 0.64 to 0.67 ms, 6.5 to 6.7 TB/s, the most that any kernel here
+// reads.
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductParams p) {
   using L = TiledLds<TOK, CH, STAGES>;
@@ -708,7 +713,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         if (tok >= m) continue;
         if (j + 4 * B <= p.rows) {
           // grouped outputs past the caches, which the weights go through (down
-          // of 4096 tokens 533 -> 524 us); aligned pieces only (3647 x 6 rows
+          // of 4096 tokens, rounding included, 533 -> 524 us when this was
+          // added, 508 now); aligned pieces only (3647 x 6 rows
           // of 731 channels 45.4 us, past the caches 52.7), and not a dense
           // product's (2608 x 1344 x 3448 40.0 us, past the caches 44.2)
           bool stored = false;
@@ -729,9 +735,12 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   }
 }
 
-// The kernels' forms, and what a product takes with each, in microseconds,
-// fitted to every form's times over dense and grouped products of 1 to 12000
-// rows (the form chosen is the fastest or within 4 % of it in the mean).
+// The kernels' forms, and what a product takes with each, in microseconds:
+// least squares on the logarithms of every form's times over dense and grouped
+// products of 1 to 12000 rows.  Over 70 others (48 of them drawn) the form
+// chosen takes 1 % longer in the mean than the fastest, 26 % at the most (the
+// down of one token: 16 x 16 15.0 us, 32 x 32 11.9).  To be fitted anew when a
+// form's kernel changes.
 // Some of them, rounding included: 4096 x 4096 x 4096: 256 x 256 tiles 76 us,
 // 128 x 256 89, 128 x 128 104, 64 x 64 167; 2000 x 2048 x 2048: 36, 28, 23, 31;
 // 500 x 4096 x 2000: 57, 42, 30, 25, direct 41; 60 x 4096 x 4096: 51, 39, 27,
@@ -751,7 +760,8 @@ constexpr TiledCost kTiledCost[kDirect32] = {
     {128, 128, 1, 0.7, 0.4, 2.5},   {64, 64, 2, 0.68, 0.3, 1.1}};
 
 // Tiles of tm rows: the counts are on the device, so every expert is taken to
-// have rows and to leave nearly half a tile empty.
+// have rows and to leave 0.42 of a tile empty (fitted: a half where counts are
+// even over a tile's height, less where some experts have no rows).
 double expected_tiles(const ProductParams& p, int tm) {
   const double n = p.n_slots;
   if (p.offsets == nullptr) return ceil(n / tm);
@@ -768,7 +778,11 @@ Form choose_form(const ProductParams& p, bool swiglu) {
   const double mean = (double)p.n_slots / p.n_experts;
   Form best = kDirect16;
   double least = 0;
-  for (int wide = 0; wide < 2; ++wide) {  // bytes of both operands from L2
+  // The direct forms: the launch and the look-up of a tile, the latency of a
+  // reduction by its length, both operands' bytes (every workgroup reads its
+  // own) at a rate of L2 that weights from HBM divide by about two, and a
+  // workgroup's start.
+  for (int wide = 0; wide < 2; ++wide) {
     const int tm = wide ? 32 : 16, strip = wide && !swiglu ? 32 : 16;
     const double groups = expected_tiles(p, tm) * ((p.rows + strip - 1) / strip);
     const double bytes = groups * p.cols * ((swiglu ? 32 : strip) + (mean < tm ? mean : tm));
@@ -787,6 +801,7 @@ Form choose_form(const ProductParams& p, bool swiglu) {
     // a dense product's tiles are known, its last round costs like a whole one
     // (4061 x 3184 x 2112: 288 tiles of 128 x 256 64 us, 144 of 256 x 256 51)
     double rounds = items / (kCus * c.per_cu);
+    // grouped, the tiles' heights differ and even the last round out to 0.3
     rounds = p.offsets == nullptr ? ceil(rounds) : rounds > 1 ? rounds + 0.3 : 1.0;
     const double us = 4.0 + rounds * (steps * (c.step + (cold ? c.cold : 0)) + c.tile);
     if (us < least) {

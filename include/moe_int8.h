@@ -18,6 +18,7 @@
  *     channels) is any size up to MOE_MAX_DIM.  int8 arrays are 16-byte
  *     aligned and without gaps between rows; scales, offsets, permutation
  *     and outputs are aligned to their element (MOE_ERR_INVALID otherwise).
+ *   - outputs do not overlap inputs.
  *   - -128 is a value like any other: the int32 sum of 65536 products cannot
  *     overflow.
  */

@@ -18,6 +18,7 @@
  *     a row may start at any multiple of its element size.  The other arrays
  *     hold 4-byte elements and are aligned to them (MOE_ERR_INVALID
  *     otherwise).
+ *   - outputs do not overlap inputs, except where a call says that they may.
  *   - hidden is any size in 1..MOE_MAX_DIM.  Sums are taken in fp32 in slot
  *     order and rounded once to the output's type, so results do not depend
  *     on scheduling.
