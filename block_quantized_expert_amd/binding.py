@@ -33,7 +33,10 @@ EXPORTED = ["moe_route", "moe_route_hash", "moe_route_group", "moe_group_workspa
             "moe_forward_ex", "moe_packed_experts_bytes", "moe_pack_experts",
             "moe_dispatch", "moe_dispatch_backward", "moe_combine", "moe_combine_backward",
             "moe_route_backward", "moe_quantize_int8", "moe_product_int8", "moe_swiglu_int8",
-            "moe_int8_form"]
+            "moe_int8_form", "moe_rmsnorm", "moe_rmsnorm_int8", "moe_rmsnorm_mxfp4",
+            "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_bytes",
+            "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_product_mxfp4",
+            "moe_swiglu_mxfp4"]
 
 WEIGHT_TYPES = {"mxfp4": MOE_W_MXFP4, "fp8_e4m3_b128": MOE_W_FP8E4M3_B128}
 
@@ -82,6 +85,20 @@ class MoeLayer(ctypes.Structure):
 class MoeInt8Weight(ctypes.Structure):
     _fields_ = [("n_experts", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
                 ("q", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
+
+
+class MoeMxfp4Weight(ctypes.Structure):
+    _fields_ = [("n_experts", ctypes.c_int32), ("rows", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p)]
+
+
+class MoeNormRows(ctypes.Structure):
+    _fields_ = [("n_rows", ctypes.c_int32), ("hidden", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("x", ctypes.c_void_p), ("x_type", ctypes.c_int32), ("x_stride", ctypes.c_int64),
+                ("weight", ctypes.c_void_p), ("w_type", ctypes.c_int32),
+                ("residual", ctypes.c_void_p), ("res_type", ctypes.c_int32),
+                ("res_stride", ctypes.c_int64), ("total", ctypes.c_void_p),
+                ("total_stride", ctypes.c_int64)]
 
 
 _lib = None
@@ -158,6 +175,21 @@ def lib() -> ctypes.CDLL:
         for name in ("moe_dispatch", "moe_dispatch_backward", "moe_combine",
                      "moe_combine_backward", "moe_route_backward", "moe_quantize_int8",
                      "moe_product_int8", "moe_swiglu_int8", "moe_int8_form"):
+            getattr(L, name).restype = ctypes.c_int
+        R, M = ctypes.POINTER(MoeNormRows), ctypes.POINTER(MoeMxfp4Weight)
+        L.moe_rmsnorm.argtypes = [R, P, I, D, P]
+        L.moe_rmsnorm_int8.argtypes = [R, P, P, P]
+        L.moe_rmsnorm_mxfp4.argtypes = [R, P, P, P]
+        L.moe_rmsnorm_backward.argtypes = [P, I, D, P, I, D, P, I, P, D, I, I, F, P, D, P, P, S, P]
+        L.moe_rmsnorm_backward_workspace_bytes.argtypes = [I, I]
+        L.moe_rmsnorm_backward_workspace_bytes.restype = S
+        L.moe_quantize_mxfp4.argtypes = [P, I, D, I, I, P, P, P]
+        L.moe_dequantize_mxfp4.argtypes = [P, P, I, I, P, I, D, P]
+        L.moe_product_mxfp4.argtypes = [M, P, P, I, P, P, I, P, I, D, P]
+        L.moe_swiglu_mxfp4.argtypes = [M, M, P, P, I, P, P, I, P, I, D, P]
+        for name in ("moe_rmsnorm", "moe_rmsnorm_int8", "moe_rmsnorm_mxfp4",
+                     "moe_rmsnorm_backward", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
+                     "moe_product_mxfp4", "moe_swiglu_mxfp4"):
             getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -539,9 +571,9 @@ def moe_forward_ex(layer: Layer, logits, x, opts, routed_scale=1.5,
 
 
 # ----------------------------------------------------------------------------
-# Rows in expert order, gradients of routing (moe_rows.h) and products in 8-bit
-# integers (moe_int8.h).  These calls check dtypes, shapes and layouts of their
-# tensors (ValueError) on top of the library's own checks; outputs that are
+# Rows in expert order, gradients of routing (moe_rows.h), products in 8-bit
+# integers (moe_int8.h), the RMS norm (moe_norm.h) and MXFP4 rows and products
+# (moe_mxfp4.h).  These calls check dtypes, shapes and layouts of their tensors (ValueError) on top of the library's own checks; outputs that are
 # not given are allocated on the call's stream.  csrc/tensor_calls.cpp holds
 # the checks.
 #
@@ -669,3 +701,99 @@ def moe_int8_form(n_experts, rows, cols, n_slots, grouped, swiglu):
     _check(lib().moe_int8_form(n_experts, rows, cols, n_slots, int(grouped), int(swiglu),
                                *[ctypes.byref(v) for v in out]), "moe_int8_form")
     return tuple(v.value for v in out)
+
+
+def moe_rmsnorm(x, weight, eps=1e-6, residual=None, total=None, y=None, y_dtype=None, stream=None):
+    """y [n][hidden], the rows of x over their root mean square times weight
+    (fp32 or bf16 [hidden]).  With a residual: (y, total), the norm of total =
+    x + residual, which is of the residual's dtype and may be the residual
+    itself.  y is of its own dtype, y_dtype or x's (the first that is given).
+    Not recorded by autograd (gradients: moe_rmsnorm_backward)."""
+    return _call("rmsnorm", stream, x, weight, eps, residual, total, y, y_dtype)
+
+
+def moe_rmsnorm_int8(x, weight, eps=1e-6, residual=None, total=None, q=None, scale=None,
+                     stream=None):
+    """moe_rmsnorm's fp32 rows rounded as moe_quantize_int8 does: (q, scale), or
+    (q, scale, total) with a residual."""
+    return _call("rmsnorm_int8", stream, x, weight, eps, residual, total, q, scale)
+
+
+def moe_rmsnorm_mxfp4(x, weight, eps=1e-6, residual=None, total=None, codes=None, scales=None,
+                      stream=None):
+    """moe_rmsnorm's fp32 rows rounded as moe_quantize_mxfp4 does: (codes,
+    scales), or (codes, scales, total) with a residual."""
+    return _call("rmsnorm_mxfp4", stream, x, weight, eps, residual, total, codes, scales)
+
+
+def moe_rmsnorm_backward(dy, s, weight, eps=1e-6, dtotal=None, dx=None, dweight=None,
+                         need_dweight=True, stream=None):
+    """(dx [n][hidden] of s's dtype, dweight fp32 [hidden]), or dx alone without
+    need_dweight and dweight.  s: the rows that were normed (total, or x without
+    a residual); dtotal: the gradient of total by its other uses, which is added
+    to dx and may be dx itself.  dx is the gradient of x and of the residual."""
+    return _call("rmsnorm_backward", stream, dy, s, weight, eps, dtotal, dx, dweight, need_dweight)
+
+
+def mxfp4_scale_rows(scales, cols):
+    """Scale words [words][n][16], as moe_quantize_mxfp4 writes them, as scale
+    bytes by rows [n][cols/32]: the order of moe.h's weights and of Mxfp4Weight's
+    argument (a copy)."""
+    words, n, _ = scales.shape
+    return scales.permute(1, 0, 2).reshape(n, words * 16)[:, :cols // 32].contiguous()
+
+
+class Mxfp4Weight:
+    """A moe_mxfp4_weight over device tensors (kept alive): ``codes`` uint8
+    [n_experts][rows][cols/2] or [rows][cols/2], ``scales`` uint8 with at least
+    cols/32 bytes a row in place of cols/2 (moe.h's order; bytes past those are
+    not looked at).  The scales are laid out anew, once, here."""
+
+    def __init__(self, codes, scales):
+        if codes.dim() == 2:
+            codes, scales = codes.unsqueeze(0), scales.unsqueeze(0)
+        if codes.dim() != 3 or codes.dtype != torch.uint8 or not codes.is_contiguous():
+            raise ValueError("codes must be a contiguous uint8 tensor of two or three dimensions")
+        e, r, c = codes.shape[0], codes.shape[1], 2 * codes.shape[2]
+        if (scales.dtype != torch.uint8 or scales.dim() != 3 or scales.shape[:2] != codes.shape[:2]
+                or scales.shape[2] < c // 32 or scales.device != codes.device):
+            raise ValueError("scales must be a uint8 tensor of shape %s or wider rows on %s"
+                             % ((e, r, c // 32), codes.device))
+        words = -(-c // 512)
+        by_row = torch.zeros((e, r, words * 16), dtype=torch.uint8, device=codes.device)
+        by_row[:, :, :c // 32] = scales[:, :, :c // 32]
+        self.codes = codes
+        self.scales = by_row.view(e, r, words, 16).transpose(1, 2).contiguous()
+        self.c = MoeMxfp4Weight(e, r, c, codes.data_ptr(), self.scales.data_ptr())
+        self.address = ctypes.addressof(self.c)
+
+    @property
+    def rows(self):
+        return self.c.rows
+
+
+def moe_quantize_mxfp4(x, codes=None, scales=None, stream=None):
+    """(codes uint8 [n][cols/2], scale words uint8 [ceil(cols/512)][n][16]) of
+    rows rounded to MXFP4."""
+    return _call("quantize_mxfp4", stream, x, codes, scales)
+
+
+def moe_dequantize_mxfp4(codes, scales, dtype=torch.bfloat16, x=None, stream=None):
+    """x [n][cols]: the values of codes and scale words."""
+    return _call("dequantize_mxfp4", stream, codes, scales, dtype, x)
+
+
+def moe_product_mxfp4(weight, codes, scales, grouping=None, top_k=0, out_dtype=torch.bfloat16,
+                      out=None, stream=None):
+    """out [slots][rows]: MXFP4 rows (codes, scale words) times the weight's
+    rows.  With a grouping, rows in expert order (top_k 0) or tokens (top_k >
+    0: every slot's token is gathered)."""
+    return _call("product_mxfp4", stream, weight.address, weight.codes, 0, None, codes, scales,
+                 grouping, top_k, out_dtype, out)
+
+
+def moe_swiglu_mxfp4(gate, up, codes, scales, grouping=None, top_k=0, out_dtype=torch.bfloat16,
+                     out=None, stream=None):
+    """SwiGLU of the gate and up products; arguments as moe_product_mxfp4."""
+    return _call("product_mxfp4", stream, gate.address, gate.codes, up.address, up.codes, codes,
+                 scales, grouping, top_k, out_dtype, out)

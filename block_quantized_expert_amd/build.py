@@ -21,7 +21,8 @@ HIPCC = os.path.join(ROCM, "bin", "hipcc")
 ARCH = "gfx950"
 
 HIP_SOURCES = ["moe_api.hip", "moe_route_group.hip", "moe_ffn.hip", "moe_gemm.hip", "moe_fused.hip",
-               "moe_pack.hip", "moe_probe.hip", "moe_rows.hip", "moe_int8.hip"]
+               "moe_pack.hip", "moe_probe.hip", "moe_rows.hip", "moe_int8.hip", "moe_norm.hip",
+               "moe_mxfp4.hip"]
 HOST_SOURCES = ["moe_host.cpp", "moe_ops_host.cpp"]
 
 COMMON = ["-O3", "-std=c++17", "-fPIC", "-Wall", "-I" + INCLUDE, "-I" + CSRC]

@@ -1,11 +1,13 @@
-// Host-side argument checks of the entry points of moe_rows.h and
-// moe_int8.h.  Pure host C++, as moe_host.h.
+// Host-side argument checks of the entry points of moe_rows.h, moe_int8.h,
+// moe_norm.h and moe_mxfp4.h.  Pure host C++, as moe_host.h.
 #pragma once
 
 #include <stddef.h>
 #include <stdint.h>
 
 #include "moe_int8.h"
+#include "moe_mxfp4.h"
+#include "moe_norm.h"
 #include "moe_rows.h"
 
 namespace moe {
@@ -33,5 +35,29 @@ moe_status check_product(const moe_int8_weight* w, const moe_int8_weight* up, co
                          const float* scale, int n_slots, const int32_t* offsets,
                          const int32_t* perm, int top_k, const void* out, int out_type,
                          int64_t out_stride);
+moe_status check_rmsnorm(const moe_norm_rows* rows, const void* y, int y_type, int64_t y_stride);
+moe_status check_rmsnorm_int8(const moe_norm_rows* rows, const int8_t* q, const float* scale);
+moe_status check_rmsnorm_mxfp4(const moe_norm_rows* rows, const uint8_t* codes,
+                               const uint8_t* scales);
+moe_status check_rmsnorm_backward(const void* dy, int dy_type, int64_t dy_stride, const void* s,
+                                  int s_type, int64_t s_stride, const void* weight, int w_type,
+                                  const void* dtotal, int64_t dtotal_stride, int n_rows,
+                                  int hidden, float eps, const void* dx, int64_t dx_stride,
+                                  const float* dweight, const void* workspace,
+                                  size_t workspace_bytes);
+// The norm's gradients: columns of a row that stays in registers, workgroups
+// that share the rows (each with a part of dweight), bytes of the longer rows'
+// r in front of those parts.
+constexpr int kNormBackCols = 8192;
+int norm_back_groups(int64_t n_rows, int hidden);
+size_t norm_inv_bytes(int64_t n_rows, int hidden);
+// Rounding and its inverse alike.
+moe_status check_mxfp4_rows(const void* x, int x_type, int64_t x_stride, int n_rows, int cols,
+                            const uint8_t* codes, const uint8_t* scales);
+// up is NULL for a plain product.
+moe_status check_product_mxfp4(const moe_mxfp4_weight* w, const moe_mxfp4_weight* up,
+                               const uint8_t* codes, const uint8_t* scales, int n_slots,
+                               const int32_t* offsets, const int32_t* perm, int top_k,
+                               const void* out, int out_type, int64_t out_stride);
 
 }  // namespace moe

@@ -1,5 +1,5 @@
-// The calls of moe_rows.h and moe_int8.h on torch tensors: argument checks,
-// outputs, the current stream, the C entry.  Their kernels take a few
+// The calls of moe_rows.h, moe_int8.h, moe_norm.h and moe_mxfp4.h on torch
+// tensors: argument checks, outputs, the current stream, the C entry.  Their kernels take a few
 // microseconds at the size of one token, where the same steps in Python took
 // three times that (one token's combine, submission: 14 us through ctypes);
 // binding.py holds the signatures and the documentation.
@@ -16,6 +16,8 @@
 #include <string>
 
 #include "moe_int8.h"
+#include "moe_mxfp4.h"
+#include "moe_norm.h"
 #include "moe_rows.h"
 
 namespace {
@@ -357,6 +359,255 @@ PyObject* product_int8(Args a) {
   return THPVariable_Wrap(o);
 }
 
+// The rows of a norm: x, weight, eps, residual, total (arguments 0 to 4); the
+// total's tensor is kept in `total`.
+struct NormArgs {
+  moe_norm_rows r{};
+  const at::Tensor &x, &w;
+  at::Tensor total;
+  NormArgs(Args a) : x(tensor(a[0], "x")), w(tensor(a[1], "weight")) {
+    const c10::Device dev = x.device();
+    TORCH_CHECK_VALUE(x.dim() == 2, "x must be a matrix");
+    const int64_t n = x.size(0), h = x.size(1);
+    r.n_rows = size(n, "x");
+    r.hidden = size(h, "hidden");
+    r.eps = number(a[2]);
+    r.x_type = act_type(x.scalar_type(), "x");
+    r.x_stride = rows_arg(x, "x", n, h, dev);
+    r.w_type = act_type(w.scalar_type(), "weight");
+    dense_arg(w, "weight", w.scalar_type(), h, dev);
+    on_gpu(dev);
+    TORCH_CHECK_VALUE(a[4] == Py_None || a[3] != Py_None, "total needs a residual");
+    if (a[3] != Py_None) {
+      const at::Tensor& res = tensor(a[3], "residual");
+      r.res_type = act_type(res.scalar_type(), "residual");
+      r.res_stride = rows_arg(res, "residual", n, h, dev);
+      r.residual = in(res);
+    }
+    r.x = in(x);
+    r.weight = in(w);
+  }
+  // with the device set
+  void open(Args a) {
+    if (a[3] == Py_None) return;
+    const int64_t n = x.size(0), h = x.size(1);
+    const at::Tensor& res = tensor(a[3], "residual");
+    total = output(a[4], "total", "the residual", {n, h}, res.scalar_type(), x.device());
+    r.total_stride = rows_arg(total, "total", n, h, x.device());
+    r.total = out(total);
+  }
+};
+
+// The outputs that there are, alone or as a tuple.
+PyObject* results(std::initializer_list<const at::Tensor*> list) {
+  PyObject* made[3];
+  Py_ssize_t n = 0;
+  bool whole = true;
+  for (const at::Tensor* t : list)
+    if (t->defined() && whole) {
+      made[n] = THPVariable_Wrap(*t);
+      whole = made[n] != nullptr;
+      n += whole;
+    }
+  if (whole && n == 1) return made[0];
+  PyObject* const r = whole ? PyTuple_New(n) : nullptr;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    if (r != nullptr)
+      PyTuple_SET_ITEM(r, i, made[i]);
+    else
+      Py_DECREF(made[i]);
+  }
+  return r;
+}
+
+// x, weight, eps, residual, total, y, y_dtype
+PyObject* rmsnorm(Args a) {
+  NormArgs v(a);
+  const c10::Device dev = v.x.device();
+  const int64_t n = v.x.size(0), h = v.x.size(1);
+  const On on(dev);
+  v.open(a);
+  const at::Tensor y =
+      a[5] != Py_None
+          ? tensor(a[5], "y")
+          : empty({n, h}, a[6] != Py_None ? dtype(a[6], "y_dtype") : v.x.scalar_type(), dev);
+  const int type = act_type(y.scalar_type(), "y");
+  const int64_t ys = rows_arg(y, "y", n, h, dev);
+  check(moe_rmsnorm(&v.r, out(y), type, ys, on.stream), "moe_rmsnorm");
+  return results({&y, &v.total});
+}
+
+// x, weight, eps, residual, total, q, scale
+PyObject* rmsnorm_int8(Args a) {
+  NormArgs v(a);
+  const c10::Device dev = v.x.device();
+  const int64_t n = v.x.size(0), h = v.x.size(1);
+  const On on(dev);
+  v.open(a);
+  const at::Tensor q = a[5] != Py_None ? tensor(a[5], "q") : empty({n, h}, at::kChar, dev);
+  const at::Tensor scale = a[6] != Py_None ? tensor(a[6], "scale") : empty({n}, at::kFloat, dev);
+  dense_arg(q, "q", at::kChar, n * h, dev);
+  dense_arg(scale, "scale", at::kFloat, n, dev);
+  check(moe_rmsnorm_int8(&v.r, out<int8_t>(q), out<float>(scale), on.stream), "moe_rmsnorm_int8");
+  return results({&q, &scale, &v.total});
+}
+
+// Codes and scale words of n rows of c columns, given or new.
+struct Mxfp4Out {
+  at::Tensor codes, scales;
+  Mxfp4Out(PyObject* given, PyObject* given_scales, int64_t n, int64_t c, c10::Device dev) {
+    const int64_t words = MOE_MXFP4_WORDS(c);
+    codes = given != Py_None ? tensor(given, "codes") : empty({n, c / 2}, at::kByte, dev);
+    scales = given_scales != Py_None ? tensor(given_scales, "scales")
+                                     : empty({words, n, 16}, at::kByte, dev);
+    dense_arg(codes, "codes", at::kByte, n * (c / 2), dev);
+    dense_arg(scales, "scales", at::kByte, words * n * 16, dev);
+  }
+};
+
+// x, weight, eps, residual, total, codes, scales
+PyObject* rmsnorm_mxfp4(Args a) {
+  NormArgs v(a);
+  const c10::Device dev = v.x.device();
+  const On on(dev);
+  v.open(a);
+  const Mxfp4Out o(a[5], a[6], v.x.size(0), v.x.size(1), dev);
+  check(moe_rmsnorm_mxfp4(&v.r, out<uint8_t>(o.codes), out<uint8_t>(o.scales), on.stream),
+        "moe_rmsnorm_mxfp4");
+  return results({&o.codes, &o.scales, &v.total});
+}
+
+// dy, s, weight, eps, dtotal, dx, dweight, need_dweight
+PyObject* rmsnorm_backward(Args a) {
+  const at::Tensor& dy = tensor(a[0], "dy");
+  const at::Tensor& s = tensor(a[1], "s");
+  const at::Tensor& w = tensor(a[2], "weight");
+  const c10::Device dev = s.device();
+  TORCH_CHECK_VALUE(s.dim() == 2, "s must be a matrix");
+  const int64_t n = s.size(0), h = s.size(1);
+  const int dy_type = act_type(dy.scalar_type(), "dy"), s_type = act_type(s.scalar_type(), "s");
+  const int w_type = act_type(w.scalar_type(), "weight");
+  const int64_t ys = rows_arg(dy, "dy", n, h, dev), ss = rows_arg(s, "s", n, h, dev);
+  dense_arg(w, "weight", w.scalar_type(), h, dev);
+  const int rows = size(n, "s"), hidden = size(h, "hidden");
+  const float eps = number(a[3]);
+  const int need = PyObject_IsTrue(a[7]);
+  if (need < 0) throw Failed();
+  on_gpu(dev);
+  const void* dtotal = nullptr;
+  int64_t ts = 0;
+  if (a[4] != Py_None) {
+    const at::Tensor& t = tensor(a[4], "dtotal");
+    TORCH_CHECK_VALUE(t.scalar_type() == s.scalar_type(), "dtotal must have s's dtype");
+    ts = rows_arg(t, "dtotal", n, h, dev);
+    dtotal = in(t);
+  }
+  const On on(dev);
+  const at::Tensor dx = output(a[5], "dx", "s", {n, h}, s.scalar_type(), dev);
+  const int64_t ds = rows_arg(dx, "dx", n, h, dev);
+  at::Tensor dw, workspace;
+  size_t bytes = 0;
+  if (a[6] != Py_None || need) {
+    dw = a[6] != Py_None ? tensor(a[6], "dweight") : empty({h}, at::kFloat, dev);
+    dense_arg(dw, "dweight", at::kFloat, h, dev);
+    bytes = moe_rmsnorm_backward_workspace_bytes(rows, hidden);
+    // freed to the stream's pool when the call returns, behind its kernels
+    workspace = empty({(int64_t)bytes}, at::kByte, dev);
+  }
+  check(moe_rmsnorm_backward(in(dy), dy_type, ys, in(s), s_type, ss, in(w), w_type, dtotal, ts, rows,
+                             hidden, eps, out(dx), ds, dw.defined() ? out<float>(dw) : nullptr,
+                             workspace.defined() ? out(workspace) : nullptr, bytes, on.stream),
+        "moe_rmsnorm_backward");
+  return results({&dx, &dw});
+}
+
+// x, codes, scales
+PyObject* quantize_mxfp4(Args a) {
+  const at::Tensor& x = tensor(a[0], "x");
+  const c10::Device dev = x.device();
+  TORCH_CHECK_VALUE(x.dim() == 2, "x must be a matrix");
+  const int64_t n = x.size(0), c = x.size(1);
+  const int type = act_type(x.scalar_type(), "x");
+  const int64_t xs = rows_arg(x, "x", n, c, dev);
+  on_gpu(dev);
+  const On on(dev);
+  const Mxfp4Out o(a[1], a[2], n, c, dev);
+  check(moe_quantize_mxfp4(in(x), type, xs, size(n, "x"), size(c, "cols"), out<uint8_t>(o.codes),
+                           out<uint8_t>(o.scales), on.stream),
+        "moe_quantize_mxfp4");
+  return pair(o.codes, o.scales);
+}
+
+// Codes [n][cols/2] and scale words [words][n][16] of a product's left operand.
+struct Mxfp4In {
+  const at::Tensor &codes, &scales;
+  int64_t n, cols;
+  c10::Device dev;
+  Mxfp4In(PyObject* c, PyObject* s)
+      : codes(tensor(c, "codes")), scales(tensor(s, "scales")), n(0), cols(0), dev(codes.device()) {
+    TORCH_CHECK_VALUE(codes.dim() == 2, "codes must be [rows][cols / 2]");
+    n = codes.size(0);
+    cols = 2 * codes.size(1);
+    dense_arg(codes, "codes", at::kByte, n * (cols / 2), dev);
+    dense_arg(scales, "scales", at::kByte, MOE_MXFP4_WORDS(cols) * n * 16, dev);
+  }
+};
+
+// codes, scales, dtype, x
+PyObject* dequantize_mxfp4(Args a) {
+  const Mxfp4In v(a[0], a[1]);
+  on_gpu(v.dev);
+  const On on(v.dev);
+  const at::Tensor x =
+      a[3] != Py_None ? tensor(a[3], "x") : empty({v.n, v.cols}, dtype(a[2], "dtype"), v.dev);
+  const int type = act_type(x.scalar_type(), "x");
+  const int64_t xs = rows_arg(x, "x", v.n, v.cols, v.dev);
+  check(moe_dequantize_mxfp4(in<uint8_t>(v.codes), in<uint8_t>(v.scales), size(v.n, "codes"),
+                             size(v.cols, "cols"), out(x), type, xs, on.stream),
+        "moe_dequantize_mxfp4");
+  return THPVariable_Wrap(x);
+}
+
+// address of the moe_mxfp4_weight and its codes, address of the up one or 0
+// and its codes or None, then codes, scales, grouping, top_k, out_dtype, out
+PyObject* product_mxfp4(Args a) {
+  const auto* w = static_cast<const moe_mxfp4_weight*>(PyLong_AsVoidPtr(a[0]));
+  const auto* up = static_cast<const moe_mxfp4_weight*>(PyLong_AsVoidPtr(a[2]));
+  if (PyErr_Occurred()) throw Failed();
+  const c10::Device wd = tensor(a[1], "the weight").device();
+  const Mxfp4In x(a[4], a[5]);
+  TORCH_CHECK_VALUE(x.cols == w->cols, "codes must be [rows][", w->cols / 2, "]");
+  TORCH_CHECK_VALUE(wd == x.dev, "the weights are on ", wd, ", codes are on ", x.dev);
+  if (up != nullptr) {
+    const c10::Device ud = tensor(a[3], "the up weight").device();
+    TORCH_CHECK_VALUE(ud == x.dev, "the up weights are on ", ud, ", codes are on ", x.dev);
+  }
+  const int k = integer(a[7], "top_k");
+  const int64_t n = x.n * (k != 0 ? k : 1), rows = w->rows;
+  Grouping g{};
+  if (a[6] != Py_None) {
+    g = grouping_arg(a[6], n, x.dev);
+    TORCH_CHECK_VALUE(g.n_experts == w->n_experts, "the grouping has ", g.n_experts,
+                      " experts, the weights ", w->n_experts);
+  }
+  on_gpu(x.dev);
+  const On on(x.dev);
+  const at::Tensor o =
+      a[9] != Py_None ? tensor(a[9], "out") : empty({n, rows}, dtype(a[8], "out_dtype"), x.dev);
+  const int type = act_type(o.scalar_type(), "out");
+  const int64_t os = rows_arg(o, "out", n, rows, x.dev);
+  const auto *codes = in<uint8_t>(x.codes), *scales = in<uint8_t>(x.scales);
+  if (up != nullptr)
+    check(moe_swiglu_mxfp4(w, up, codes, scales, size(n, "codes"), g.offsets, g.perm, k, out(o),
+                           type, os, on.stream),
+          "moe_swiglu_mxfp4");
+  else
+    check(moe_product_mxfp4(w, codes, scales, size(n, "codes"), g.offsets, g.perm, k, out(o), type,
+                            os, on.stream),
+          "moe_product_mxfp4");
+  return THPVariable_Wrap(o);
+}
+
 template <PyObject* (*F)(Args), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   HANDLE_TH_ERRORS
@@ -386,6 +637,13 @@ PyMethodDef methods[] = {method<set_error, 1>("set_error"),
                          method<route_backward, 6>("route_backward"),
                          method<quantize_int8, 3>("quantize_int8"),
                          method<product_int8, 10>("product_int8"),
+                         method<rmsnorm, 7>("rmsnorm"),
+                         method<rmsnorm_int8, 7>("rmsnorm_int8"),
+                         method<rmsnorm_mxfp4, 7>("rmsnorm_mxfp4"),
+                         method<rmsnorm_backward, 8>("rmsnorm_backward"),
+                         method<quantize_mxfp4, 3>("quantize_mxfp4"),
+                         method<dequantize_mxfp4, 4>("dequantize_mxfp4"),
+                         method<product_mxfp4, 10>("product_mxfp4"),
                          {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "tensor_calls", nullptr, -1, methods,
