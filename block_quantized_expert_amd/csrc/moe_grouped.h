@@ -118,6 +118,97 @@ __device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
 constexpr int kTableSpan = MOE_MAX_EXPERTS / kWave + 1;
 constexpr int kCus = 256;
 
+// The tiles in front of each expert's, TOK rows a tile at most, by the
+// workgroup's first wavefront: first[0 .. n_experts] in LDS.
+template <int TOK>
+__device__ __forceinline__ void tile_table(const GroupedRows& p, int32_t* first) {
+  const int lane = threadIdx.x % kWave;
+  const bool grouped = p.offsets != nullptr;
+  const int n_exp = grouped ? p.n_experts : 1;
+  int off[kTableSpan + 1], sum = 0;
+  if (grouped) {
+#pragma unroll
+    for (int i = 0; i <= kTableSpan; ++i) off[i] = p.offsets[min(lane * kTableSpan + i, n_exp)];
+#pragma unroll
+    for (int i = 0; i <= kTableSpan; ++i) off[i] = min(max(off[i], 0), p.n_slots);
+  } else {
+#pragma unroll
+    for (int i = 0; i <= kTableSpan; ++i) off[i] = lane + i == 0 ? 0 : p.n_slots;
+  }
+#pragma unroll
+  for (int i = 0; i < kTableSpan; ++i) sum += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
+  int incl = sum;
+#pragma unroll
+  for (int s = 1; s < kWave; s <<= 1) {
+    const int v = __shfl_up(incl, s);
+    if (lane >= s) incl += v;
+  }
+  int at = incl - sum;
+#pragma unroll
+  for (int i = 0; i < kTableSpan; ++i) {
+    const int e = lane * kTableSpan + i;
+    if (e <= n_exp) first[e] = at;
+    at += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
+  }
+}
+
+// An expert's first row, through the scalar cache: a vector load's wait would
+// drain the copies in flight.
+__device__ __forceinline__ int offset_of(const GroupedRows& p, int e) {
+  if (p.offsets == nullptr) return e == 0 ? 0 : p.n_slots;
+  return min(max(((scalar_i32)(uintptr_t)p.offsets)[e], 0), p.n_slots);
+}
+
+// One item of a tiled product: a tile of rows and a strip of channels.
+struct Item {
+  int expert, row0, m;  // m rows from row0 on
+  int j0;               // the strip's first channel
+  bool only;            // its expert's only tile
+};
+
+// Token tiles that follow one another under one strip of channels: the strip
+// is then read from memory once and by the others from L2.
+constexpr int kTileGroup = 4;
+
+// Item `index` of the table's tiles times `strips`.  Every lane of the
+// wavefront calls this.
+template <int TOK>
+__device__ __forceinline__ Item find_item(const GroupedRows& p, const int32_t* first,
+                                          uint32_t index, uint32_t strips, int strip_channels) {
+  const int lane = threadIdx.x % kWave;
+  const int n_exp = p.offsets != nullptr ? p.n_experts : 1;
+  const int t = (int)(index / strips);
+  const int a = __popcll(__ballot(first[min(lane * kTableSpan, n_exp)] <= t)) - 1;
+  const int e1 = min(a * kTableSpan + lane, n_exp);
+  const int e = a * kTableSpan + __popcll(__ballot(lane < kTableSpan && first[e1] <= t)) - 1;
+  Item it;
+  it.expert = __builtin_amdgcn_readfirstlane(e);
+  const uint32_t f = __builtin_amdgcn_readfirstlane(first[it.expert]);
+  const uint32_t tiles = __builtin_amdgcn_readfirstlane(first[it.expert + 1]) - f;
+  it.only = tiles == 1;
+  const uint32_t rem = index - f * strips;
+  const uint32_t grp = rem / (kTileGroup * strips);
+  const uint32_t in = rem - grp * (kTileGroup * strips);
+  const uint32_t n = min((uint32_t)kTileGroup, tiles - grp * kTileGroup);
+  const int tile = grp * kTileGroup + in % n;
+  it.j0 = in / n * strip_channels;
+  const int lo = offset_of(p, it.expert), hi = offset_of(p, it.expert + 1);
+  it.row0 = lo + tile * TOK;
+  it.m = min(TOK, hi - it.row0);
+  return it;
+}
+
+// The items of workgroup b of a persistent grid: it runs on XCD b % 8, which
+// takes one contiguous eighth of the items; begin, begin + step, ... below end.
+struct Share {
+  uint32_t begin, step, end;
+};
+__device__ __forceinline__ Share share_of(uint32_t items) {
+  const uint32_t xcd = blockIdx.x % 8;
+  return {(uint32_t)((uint64_t)items * xcd / 8) + blockIdx.x / 8, gridDim.x / 8,
+          (uint32_t)((uint64_t)items * (xcd + 1) / 8)};
+}
+
 // This wavefront's copies into LDS are done but for the newest N and its LDS
 // reads are complete (the compiler may place the barrier above the products
 // that use them), then the workgroup's barrier.  Not __syncthreads(), whose

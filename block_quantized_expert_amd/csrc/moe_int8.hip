@@ -224,10 +224,6 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
 
 // ------------------------------------------------------------- tiled products
 
-// Token tiles that follow one another under one strip of channels: the strip
-// is then read from memory once and by the others from L2.
-constexpr int kTileGroup = 4;
-
 // LDS: STAGES steps of weights [CH][128] and rows [TOK][128], then kSlots
 // tiles' scales (of the CH weight rows, and of the rows eight times each, as
 // the copies place them), then the tiles in front of each expert's.  A tile's
@@ -282,41 +278,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   const int wt = wave % WT, wc = wave / WT;
   const bool grouped = p.offsets != nullptr;
   const int n_exp = grouped ? p.n_experts : 1;
-  const scalar_i32 offs = (scalar_i32)(uintptr_t)p.offsets;
-
-  auto offset_of = [&](int e) -> int {
-    if (!grouped) return e == 0 ? 0 : p.n_slots;
-    return min(max(offs[e], 0), p.n_slots);
-  };
-
-  // tiles in front of each expert's
-  if (wave == 0) {
-    int off[kTableSpan + 1], sum = 0;
-    if (grouped) {
-#pragma unroll
-      for (int i = 0; i <= kTableSpan; ++i) off[i] = p.offsets[min(lane * kTableSpan + i, n_exp)];
-#pragma unroll
-      for (int i = 0; i <= kTableSpan; ++i) off[i] = min(max(off[i], 0), p.n_slots);
-    } else {
-#pragma unroll
-      for (int i = 0; i <= kTableSpan; ++i) off[i] = lane + i == 0 ? 0 : p.n_slots;
-    }
-#pragma unroll
-    for (int i = 0; i < kTableSpan; ++i) sum += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
-    int incl = sum;
-#pragma unroll
-    for (int s = 1; s < kWave; s <<= 1) {
-      const int v = __shfl_up(incl, s);
-      if (lane >= s) incl += v;
-    }
-    int at = incl - sum;
-#pragma unroll
-    for (int i = 0; i < kTableSpan; ++i) {
-      const int e = lane * kTableSpan + i;
-      if (e <= n_exp) first[e] = at;
-      at += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
-    }
-  }
+  if (wave == 0) tile_table<TOK>(p, first);
   __syncthreads();
   const uint32_t strips = (p.rows + kStripCh - 1) / kStripCh;
   const uint32_t items = (uint32_t)first[n_exp] * strips;
@@ -324,38 +286,14 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   // rows without an expert
   if (grouped) {
     O* out = static_cast<O*>(p.out);
-    for (int64_t r = (int64_t)offset_of(n_exp) + blockIdx.x; r < p.n_slots; r += gridDim.x)
+    for (int64_t r = (int64_t)offset_of(p, n_exp) + blockIdx.x; r < p.n_slots; r += gridDim.x)
       for (int j = threadIdx.x; j < p.rows; j += kWave * NW)
         out[r * p.out_stride + j] = static_cast<O>(0.0f);
   }
 
-  // item `index`: expert, first row, rows and first channel; is it its expert's only tile
-  auto find = [&](uint32_t index, int& expert, int& row0, int& m, int& j0, bool& only) {
-    const int t = (int)(index / strips);
-    const int a = __popcll(__ballot(first[min(lane * kTableSpan, n_exp)] <= t)) - 1;
-    const int e1 = min(a * kTableSpan + lane, n_exp);
-    const int e = a * kTableSpan + __popcll(__ballot(lane < kTableSpan && first[e1] <= t)) - 1;
-    expert = __builtin_amdgcn_readfirstlane(e);
-    const uint32_t f = __builtin_amdgcn_readfirstlane(first[expert]);
-    const uint32_t tiles = __builtin_amdgcn_readfirstlane(first[expert + 1]) - f;
-    only = tiles == 1;
-    const uint32_t rem = index - f * strips;
-    const uint32_t grp = rem / (kTileGroup * strips);
-    const uint32_t in = rem - grp * (kTileGroup * strips);
-    const uint32_t n = min((uint32_t)kTileGroup, tiles - grp * kTileGroup);
-    const int tile = grp * kTileGroup + in % n;
-    j0 = in / n * kStripCh;
-    const int lo = offset_of(expert), hi = offset_of(expert + 1);
-    row0 = lo + tile * TOK;
-    m = min(TOK, hi - row0);
-  };
-
-  // this workgroup's items: workgroup b runs on XCD b % 8, which takes one
-  // contiguous eighth of the items
-  const uint32_t xcd = blockIdx.x % 8, per = gridDim.x / 8;
-  const uint32_t end = (uint32_t)((uint64_t)items * (xcd + 1) / 8);
-  uint32_t load_item = (uint32_t)((uint64_t)items * xcd / 8) + blockIdx.x / 8;
-  uint32_t item = load_item;
+  const Share share = share_of(items);
+  const uint32_t per = share.step, end = share.end;
+  uint32_t load_item = share.begin, item = load_item;
   const int ksteps = (p.cols + 127) / 128;
   const int tail = p.cols % 128 != 0 ? ksteps - 1 : -1;
 
@@ -379,8 +317,9 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     return b < CB / 2 ? 0 : 1;
   };
   auto open = [&]() {
-    int expert, row0, m, j0;
-    find(load_item, expert, row0, m, j0, once);
+    const Item it = find_item<TOK>(p, first, load_item, strips, kStripCh);
+    const int expert = it.expert, row0 = it.row0, m = it.m, j0 = it.j0;
+    once = it.only;
     char* const slot = smem + L::kScales + load_slot * L::kSlot;
     load_slot = load_slot + 1 == L::kSlots ? 0 : load_slot + 1;
     if (wave < CH / kWave) {
@@ -503,9 +442,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
                     p.out_stride * sizeof(O) % 16 == 0;
   int slot = 0;
   for (; item < end; item += per) {
-    int expert, row0, m, j0;
-    bool only;
-    find(item, expert, row0, m, j0, only);
+    const Item it = find_item<TOK>(p, first, item, strips, kStripCh);
+    const int row0 = it.row0, m = it.m, j0 = it.j0;
     // blocks with rows
     const int live =
         kSkip ? __builtin_amdgcn_readfirstlane(((m + 15) / 16 - wt + WT - 1) / WT) : TB;

@@ -146,9 +146,8 @@ __device__ __forceinline__ f32x4 mfma_fp4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, c, 4, 4, 0, (int)sa, 0, (int)sb);
 }
 
-struct alignas(8) Scales8 {  // of 256 inputs
-  uint32_t v[2];
-};
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));  // scale bytes of 256 inputs
+typedef uint32_t u32x1 __attribute__((ext_vector_type(1)));
 
 // Small products: 16 TB rows x 16 CB channels a workgroup (SwiGLU: CB 1, gate
 // and up), the reduction dealt to the wavefronts in turns of 256 inputs,
@@ -200,7 +199,7 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
     auto turns = [&](int k0, auto count, auto whole) {
       constexpr int C = decltype(count)::value;
       u32x4 wv[C][2][M], xv[C][2][TB];
-      Scales8 wsv[C][M], xsv[C][TB];
+      u32x2 wsv[C][M], xsv[C][TB];
 #pragma unroll
       for (int c = 0; c < C; ++c) {
         const int k = k0 + c * kWaves * 128;
@@ -208,10 +207,10 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
         const int half = k / 128 % 2 * 8;
 #pragma unroll
         for (int i = 0; i < M; ++i)
-          wsv[c][i] = *reinterpret_cast<const Scales8*>(ws[i] + word * p.rows * 16 + half);
+          wsv[c][i] = *reinterpret_cast<const u32x2*>(ws[i] + word * p.rows * 16 + half);
 #pragma unroll
         for (int b = 0; b < TB; ++b)
-          xsv[c][b] = *reinterpret_cast<const Scales8*>(xs[b] + word * p.left_rows * 16 + half);
+          xsv[c][b] = *reinterpret_cast<const u32x2*>(xs[b] + word * p.left_rows * 16 + half);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const bool in = decltype(whole)::value || k + 64 * h + 16 * g < row_bytes;
@@ -231,8 +230,8 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
           for (int i = 0; i < M; ++i)
 #pragma unroll
             for (int b = 0; b < TB; ++b)
-              acc[i][b] = mfma_fp4(wv[c][h][i], xv[c][h][b], acc[i][b], wsv[c][i].v[h] >> (8 * g),
-                                   xsv[c][b].v[h] >> (8 * g));
+              acc[i][b] = mfma_fp4(wv[c][h][i], xv[c][h][b], acc[i][b], wsv[c][i][h] >> (8 * g),
+                                   xsv[c][b][h] >> (8 * g));
     };
     int k0 = wave * 128;
     for (; k0 + (kTurns - 1) * kWaves * 128 + 128 <= row_bytes; k0 += kTurns * kWaves * 128)
@@ -267,6 +266,403 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
   }
 }
 
+// ------------------------------------------------------------- tiled products
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// D = A * B + C on 32x32x64 E2M1 values; lane l: row l % 32 of A and column l %
+// 32 of B, inputs 32 (l / 32) .. +31 under byte S of its scales.  The result
+// lane l holds D[8 (i / 4) + 4 (l / 32) + i % 4][l % 32] for i = 0..15.  Twice
+// the rate of 16x16x128 (8.5 against 4.4 PFLOP/s of instructions alone), so
+// the tiles are built from it.  The sum is as good as one in fp32: 2^-20 of the
+// largest term or sum where the scales lie thirty binades apart, exact where
+// the terms fit 24 bits together (checked on the hardware against 64 bits).
+template <int S>
+__device__ __forceinline__ f32x16 mfma_fp4_32(u32x4 a, u32x4 b, f32x16 c, uint32_t sa,
+                                              uint32_t sb) {
+  const i32x8 av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+  const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
+  return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
+}
+
+// LDS: STAGES steps of weights [CH][128] and rows [TOK][128], STAGES slots of
+// scale words, then the tiles in front of each expert's.  A slot holds one
+// 16-byte word for every row of a step and the next, in the order of the
+// copies: of each wavefront's rows, then of its weight rows.  It is copied with
+// its first step; the word STAGES words before has its last step at least
+// STAGES steps before, which every wavefront has left by then.
+template <int TOK, int CH, int NW, int STAGES>
+struct TiledLds {
+  static constexpr int kW = CH / 8 / NW;                          // copies of weights a step
+  static constexpr int kX = TOK / 8 / NW > 0 ? TOK / 8 / NW : 1;  // and of rows
+  static constexpr int kStage = (TOK + CH) * 128;
+  static constexpr int kScales = STAGES * kStage;
+  static constexpr int kWave8 = 8 * (kX + kW);  // words a wavefront copies
+  static constexpr int kSlot = NW * 16 * kWave8;
+  static constexpr int kTable = kScales + STAGES * kSlot;
+  static constexpr int kBytes = kTable + 4 * (MOE_MAX_EXPERTS + 2);
+  static_assert(kWave8 <= kWave && 32 % (8 * kX) == 0 && 32 % (8 * kW) == 0, "scale words");
+};
+
+// Large products: TOK rows x CH rows of weights (SwiGLU: gate and up of CH / 2
+// channels, sixteen of each a matrix instruction) a workgroup of WT x WC
+// wavefronts, the reduction in steps of 128 bytes of a row, 256 inputs.  Both
+// operands go from memory into LDS by asynchronous 16-byte copies, STAGES - 1
+// steps ahead and across the end of a tile, so a workgroup that goes from tile
+// to tile never waits for a first load; LDS also turns whole 128-byte lines of
+// memory into the matrix instruction's layout.  A word of scales serves two
+// steps of a row, and a wavefront copies those of all its rows at once.
+template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
+__global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductParams p) {
+  constexpr int NW = WT * WC;
+  using L = TiledLds<TOK, CH, NW, STAGES>;
+  constexpr int CB = CH / WC / 32, TB = TOK / WT / 32;
+  constexpr int kW = L::kW, kX = L::kX;
+  constexpr int kStripCh = SWIGLU ? CH / 2 : CH;
+  extern __shared__ char smem[];
+  int32_t* const first = reinterpret_cast<int32_t*>(smem + L::kTable);
+  const int lane = threadIdx.x % kWave;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int r32 = lane % 32, half = lane / 32;
+  const int wt = wave % WT, wc = wave / WT;
+  const bool grouped = p.offsets != nullptr;
+  const int n_exp = grouped ? p.n_experts : 1;
+  if (wave == 0) tile_table<TOK>(p, first);
+  __syncthreads();
+  const uint32_t strips = (p.rows + kStripCh - 1) / kStripCh;
+  const uint32_t items = (uint32_t)first[n_exp] * strips;
+
+  // rows without an expert
+  if (grouped) {
+    O* out = static_cast<O*>(p.out);
+    for (int64_t r = (int64_t)offset_of(p, n_exp) + blockIdx.x; r < p.n_slots; r += gridDim.x)
+      for (int j = threadIdx.x; j < p.rows; j += kWave * NW)
+        out[r * p.out_stride + j] = static_cast<O>(0.0f);
+  }
+
+  const Share share = share_of(items);
+  const uint32_t per = share.step, end = share.end;
+  uint32_t load_item = share.begin, item = load_item;
+  const int row_bytes = p.cols / 2;
+  const int ksteps = (row_bytes + 127) / 128;
+  const int tail = row_bytes % 128 != 0 ? ksteps - 1 : -1;
+
+  // Copies into LDS.  One copies 8 rows of 128 bytes; a lane's chunk is the
+  // one that belongs at its place: chunk c of row r lies at c ^ (r / 2 % 8),
+  // so that sixteen rows of an operand read meet different banks.
+  // Weights: a matrix of at most 2^31 bytes, an offset a lane.
+  const uint8_t* wbase[SWIGLU ? 2 : 1];  // of the item's expert, advanced by steps
+  uint32_t woffset[kW] = {};
+#pragma unroll
+  for (int m = 0; m < (SWIGLU ? 2 : 1); ++m) wbase[m] = p.w[m];
+  const uint8_t* xsrc[kX];
+  const uint8_t* ssrc = nullptr;  // the scale word of lane: its rows' first, then its weights'
+  const int chunk_even = (lane % 8) ^ (lane / 16);  // rows 8j + lane / 8 of even j
+  const bool scale_x = lane < 8 * kX;
+  const int64_t scale_step = (int64_t)(scale_x ? p.left_rows : p.rows) * 16;
+  int load_step = 0, into = 0, scale_into = 0;
+  auto x_copy = [&](int i) { return (wave * kX + i) % (TOK / 8); };
+  // LDS row r of the weights: its matrix and channel
+  auto weight_row = [&](int r, int j0, int& ch) {
+    if (!SWIGLU) {
+      ch = min(j0 + r, p.rows - 1);
+      return 0;
+    }
+    ch = min(j0 + r / 32 * 16 + r % 16, p.rows - 1);
+    return r / 16 % 2;
+  };
+  auto open = [&]() {
+    const Item it = find_item<TOK>(p, first, load_item, strips, kStripCh);
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+      const int j = wave * kW + i;
+      const int chunk = chunk_even ^ (4 * (j & 1));
+      int ch;
+      weight_row(8 * j + lane / 8, it.j0, ch);
+      woffset[i] = (uint32_t)ch * row_bytes + 16 * chunk;
+    }
+#pragma unroll
+    for (int m = 0; m < (SWIGLU ? 2 : 1); ++m)
+      wbase[m] = p.w[m] + (int64_t)it.expert * p.rows * row_bytes;
+    int scale_row = 0;
+#pragma unroll
+    for (int i = 0; i < kX; ++i) {
+      const int j = x_copy(i);
+      const int chunk = chunk_even ^ (4 * (j & 1));
+      int row = it.row0 + min(8 * j + lane / 8, it.m - 1);
+      if (p.top_k != 0) {
+        // through the scalar cache: a vector load's wait would drain the copies in flight
+        const scalar_i32 perm = (scalar_i32)(uintptr_t)p.perm;
+        int f = 0;
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int v = perm[it.row0 + min(8 * j + r, it.m - 1)];
+          f = lane / 8 == r ? v : f;
+        }
+        row = f >= 0 && f < p.n_slots ? f / p.top_k : 0;
+      }
+      xsrc[i] = p.x + (int64_t)row * row_bytes + 16 * chunk;
+      // row 8i + r of this wavefront's is at lanes 8r .. 8r + 7
+      const int r = __shfl(row, 8 * (lane % 8));
+      scale_row = lane / 8 == i ? r : scale_row;
+    }
+    if (scale_x) {
+      ssrc = p.x_scales + (int64_t)scale_row * 16;
+    } else {
+      int ch;
+      const int r = wave * 8 * kW + min(lane - 8 * kX, 8 * kW - 1);
+      const uint8_t* ws = p.w_scales[0];
+      if (weight_row(r, it.j0, ch) != 0) ws = p.w_scales[1];
+      ssrc = ws + ((int64_t)it.expert * p.words * p.rows + ch) * 16;
+    }
+  };
+  // the scale words of the next step and the one after it
+  auto copy_scales = [&]() {
+    if (lane < L::kWave8)
+      __builtin_amdgcn_global_load_lds(
+          ssrc,
+          (__attribute__((address_space(3))) void*)(smem + L::kScales + scale_into * L::kSlot +
+                                                    wave * 16 * L::kWave8),
+          16, 0, 0);
+    ssrc += scale_step;
+    scale_into = scale_into + 1 == STAGES ? 0 : scale_into + 1;
+  };
+  // copy i of the next step into buffer b, and the step's end
+  auto copy = [&](int i, int b) {
+    const bool w = i < kW;
+    const int j = w ? wave * kW + i : x_copy(i - kW);
+    const auto to = (__attribute__((address_space(3))) void*)(smem + b * L::kStage +
+                                                            ((w ? 0 : CH) + 8 * j) * 128);
+    if (w) {
+      // 16 rows of a matrix in turn
+      const uint8_t* const src = wbase[SWIGLU ? j / 2 % 2 : 0] + woffset[w ? i : 0];
+      __builtin_amdgcn_global_load_lds(src, to, 16, 0, 0);
+    } else {
+      const uint8_t*& src = xsrc[w ? 0 : i - kW];
+      __builtin_amdgcn_global_load_lds(src, to, 16, 0, 0);
+      src += 128;
+    }
+  };
+  // What comes in front of a step's copies: a tile's first rows, the words of
+  // scales, and zeros of the rows instead of what lies past their end (the
+  // weights' first bytes of the step then, which zeros multiply).  Behind the last item
+  // the copies go on, with zeros and weights that nothing uses, so that every
+  // step has as many and no branch stands between its products.
+  auto begin_step = [&]() {
+    const bool more = load_item < end;
+    if (more && load_step == 0) open();
+    if (more && load_step % 2 == 0) copy_scales();
+    if (more && load_step != tail) return;
+#pragma unroll
+    for (int i = 0; i < kW + kX; ++i) {
+      const int j = i < kW ? wave * kW + i : x_copy(i - kW);
+      const int chunk = chunk_even ^ (4 * (j & 1));
+      if (more && load_step * 128 + 16 * chunk < row_bytes) continue;
+      if (i < kW)
+        woffset[i < kW ? i : 0] -= more ? 16 * chunk : 0;
+      else
+        xsrc[i < kW ? 0 : i - kW] = reinterpret_cast<const uint8_t*>(&kZeroChunk);
+    }
+  };
+  // Without a branch: the compiler would move products past it.
+  auto copied = [&]() {
+    into = into + 1 == STAGES ? 0 : into + 1;
+    const bool more = load_item < end, last = load_step + 1 == ksteps;
+#pragma unroll
+    for (int m = 0; m < (SWIGLU ? 2 : 1); ++m) wbase[m] += more && !last ? 128 : 0;
+    load_step = more && !last ? load_step + 1 : 0;
+    load_item += more && last ? per : 0;
+  };
+
+  for (int i = 0; i < STAGES - 1; ++i) {
+    begin_step();
+#pragma unroll
+    for (int c = 0; c < kW + kX; ++c) copy(c, into);
+    copied();
+  }
+
+  const int swz = 16 * (half ^ (r32 / 2 % 8));
+  const int woff = (wc * CB * 32 + r32) * 128 + swz;
+  const int xoff = (CH + wt * 32 + r32) * 128 + swz;  // its blocks of rows: every WT-th
+  auto scale_at = [&](int r, int each, int at) {
+    return (r / (8 * each) * L::kWave8 + at + r % (8 * each)) * 16;
+  };
+  const int wscale = scale_at(wc * CB * 32 + r32, kW, 8 * kX);
+  const int xscale = scale_at(wt * 32 + r32, kX, 0);
+  // A step is 4 TB units: a quarter's 64 inputs, one block of 32 rows, all
+  // blocks of weights.  Operands are read two units ahead, the first of a
+  // step before the step in front of it ends.
+  constexpr int U = 4 * TB;
+  constexpr int kWRing = TB > 1 ? 2 : 4;
+  constexpr int kCopies = kW + kX;
+  u32x4 wv[kWRing][CB], xv[4];
+  uint32_t ws[2][CB], xs[2][TB];  // scale bytes of the step's first and second 128 inputs
+  auto read_w = [&](const char* buf, int h) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      wv[h % kWRing][c] = *reinterpret_cast<const u32x4*>(buf + (woff ^ (32 * h)) + c * 4096);
+  };
+  auto read_x = [&](const char* buf, int u) {
+    xv[u % 4] = *reinterpret_cast<const u32x4*>(buf + (xoff ^ (32 * (u / TB))) + u % TB * WT * 4096);
+  };
+  int from = STAGES - 1, scale_from = STAGES - 1;
+  // the bytes of blocks 2h and 2h + 1 are 2h % 4 and 2h % 4 + 1 of the word's part h / 2; the
+  // upper lanes take the second
+  const char* scales = nullptr;
+  auto read_scales = [&](int d) {
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      ws[d][c] = (*reinterpret_cast<const u32x1*>(scales + wscale + 4 * d +
+                                                  c * 32 / (8 * kW) * L::kWave8 * 16))[0];
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+      xs[d][t] = (*reinterpret_cast<const u32x1*>(scales + xscale + 4 * d +
+                                                  t * WT * 32 / (8 * kX) * L::kWave8 * 16))[0];
+  };
+  // the next step's copies have landed, and every wavefront has read this
+  // step's operands: the buffer is free
+  auto next_step = [&](int step) {
+    step_barrier<(STAGES - 2) * kCopies>();
+    from = from + 1 == STAGES ? 0 : from + 1;
+    if (step % 2 == 0) scale_from = scale_from + 1 == STAGES ? 0 : scale_from + 1;
+    const char* const buf = smem + from * L::kStage;
+    scales = smem + L::kScales + scale_from * L::kSlot + step % 2 * 8;
+    read_scales(0);
+    read_w(buf, 0);
+    read_x(buf, 0);
+    read_x(buf, 1);
+    if (TB == 1) read_w(buf, 1);
+  };
+  next_step(0);
+  const bool past = grouped && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
+                    p.out_stride * sizeof(O) % 16 == 0;
+  for (; item < end; item += per) {
+    const Item it = find_item<TOK>(p, first, item, strips, kStripCh);
+    f32x16 acc[CB][TB];
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+#pragma unroll
+      for (int t = 0; t < TB; ++t)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc[c][t][i] = 0.0f;
+    for (int ks = 0; ks < ksteps; ++ks) {
+      begin_step();
+      const char* const buf = smem + from * L::kStage;
+      read_scales(1);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int h = u / TB, t = u % TB;
+        if (TB > 1 && h < 3 && t == (TB > 2 ? TB - 2 : 0)) read_w(buf, h + 1);
+        if (TB == 1 && u + 2 < U) read_w(buf, u + 2);
+        if (u + 2 < U) read_x(buf, u + 2);
+        // copies go between the products: a copy waits at its issue while the
+        // CU has as many lines in flight as it can
+        constexpr int kSpan = STAGES == 2 ? U / 2 : U - 2;
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i)
+          if (i * kSpan / kCopies == u) copy(i, into);
+        if (u == U - 2) {
+          copied();
+          next_step(ks + 1 == ksteps ? 0 : ks + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (h % 2 == 0) {
+          if (t == 0)
+#pragma unroll
+            for (int c = 0; c < CB; ++c) ws[h / 2][c] >>= 8 * half;
+          xs[h / 2][t] >>= 8 * half;
+        }
+#pragma unroll
+        for (int c = 0; c < CB; ++c)
+          acc[c][t] = h % 2 == 0 ? mfma_fp4_32<0>(wv[h % kWRing][c], xv[u % 4], acc[c][t],
+                                                  ws[h / 2][c], xs[h / 2][t])
+                                 : mfma_fp4_32<2>(wv[h % kWRing][c], xv[u % 4], acc[c][t],
+                                                  ws[h / 2][c], xs[h / 2][t]);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    // lane: token r32, channels 8q + 4 half .. + 3 of a block's quarter q; of
+    // SwiGLU the gate's are quarters 0 and 1, the up's of the same channels 2 and 3
+    constexpr int Q = SWIGLU ? 2 : 4;
+#pragma unroll
+    for (int t = 0; t < TB; ++t) {
+      const int tok = (t * WT + wt) * 32 + r32;
+      O* const out = static_cast<O*>(p.out) + (it.row0 + (int64_t)tok) * p.out_stride;
+      // Two quarters' bf16 values change hands between the wavefront's halves,
+      // so that a lane stores 16 bytes.
+      constexpr int N = sizeof(O) == 2 ? 2 : 1;
+#pragma unroll
+      for (int c = 0; c < CB; ++c)
+#pragma unroll
+        for (int q = 0; q < Q; q += N) {
+          struct alignas(16) {
+            O v[4 * N];
+          } o;
+#pragma unroll
+          for (int i = 0; i < 4 * N; ++i)
+            o.v[i] = finish<SWIGLU, O>(acc[c][t][4 * q + i], acc[c][t][SWIGLU ? 8 + 4 * q + i : 0]);
+          int j = it.j0 + (wc * CB + c) * 8 * Q + 8 * q + 4 * half;
+          if constexpr (N == 2) {
+            uint32_t w[4];
+            __builtin_memcpy(w, o.v, sizeof(w));
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const auto r = __builtin_amdgcn_permlane32_swap(w[i], w[2 + i], false, false);
+              w[i] = r[0];
+              w[2 + i] = r[1];
+            }
+            __builtin_memcpy(o.v, w, sizeof(w));
+            j += 4 * half;
+          }
+          if (tok >= it.m) continue;
+          if (j + 4 * N <= p.rows) {
+            // grouped outputs past the caches, which the weights go through
+            if (past)
+              __builtin_nontemporal_store(__builtin_bit_cast(u32x4, o),
+                                          reinterpret_cast<u32x4*>(out + j));
+            else
+              __builtin_memcpy(out + j, o.v, 16);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4 * N; ++i)
+              if (j + i < p.rows) out[j + i] = o.v[i];
+          }
+        }
+    }
+  }
+  __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy outlives the workgroup's LDS
+}
+
+// The kernels' forms.
+enum Form { k256x256, k128x256, k64x256, k32x256, k128x128, k64x64, kDirect32, kDirect16 };
+struct TiledShape {
+  int rows, ch;  // tile (SwiGLU: of ch / 2 channels)
+  int per_cu;    // workgroups on a CU
+};
+constexpr TiledShape kTiled[kDirect32] = {{256, 256, 1}, {128, 256, 1}, {64, 256, 1},
+                                          {32, 256, 1},  {128, 128, 1}, {64, 64, 2}};
+
+template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
+hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) {
+  using L = TiledLds<TOK, CH, WT * WC, STAGES>;
+  static_assert(L::kBytes <= 160 * 1024, "LDS");
+  constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
+  static const hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kernel, dim3(kCus * per_cu), dim3(kWave * WT * WC), L::kBytes, stream, p);
+  return hipGetLastError();
+}
+
+Form choose_form(const ProductParams& p, bool swiglu) {
+  const double mean = (double)p.n_slots / p.n_experts;
+  if (mean <= 16 || p.n_slots <= 32) return kDirect16;
+  if (mean <= 32) return k32x256;
+  if (mean <= 64) return k64x256;
+  if (mean <= 128) return k128x256;
+  return k256x256;
+}
+
 template <bool SWIGLU, typename O, int TB, int CB>
 void launch_direct(ProductParams p, hipStream_t stream) {
   const int64_t tiles = p.max_tiles = max_tiles(p, 16 * TB);
@@ -281,7 +677,17 @@ void launch_direct(ProductParams p, hipStream_t stream) {
 
 template <bool SWIGLU, typename O>
 hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
-  launch_direct<SWIGLU, O, 1, 1>(p, stream);
+  const Form f = choose_form(p, SWIGLU);
+  switch (f) {
+    case k256x256: return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, 1, stream);
+    case k128x256: return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 2>(p, 1, stream);
+    case k64x256: return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, 1, stream);
+    case k32x256: return launch_tiled<SWIGLU, O, 32, 256, 1, 8, 3>(p, 1, stream);
+    case k128x128: return launch_tiled<SWIGLU, O, 128, 128, 2, 4, 4>(p, 1, stream);
+    case k64x64: return launch_tiled<SWIGLU, O, 64, 64, 2, 2, 3>(p, 2, stream);
+    case kDirect32: launch_direct<SWIGLU, O, 2, SWIGLU ? 1 : 2>(p, stream); break;
+    default: launch_direct<SWIGLU, O, 1, 1>(p, stream);
+  }
   return hipGetLastError();
 }
 
