@@ -285,24 +285,58 @@ __device__ __forceinline__ f32x16 mfma_fp4_32(u32x4 a, u32x4 b, f32x16 c, uint32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, c, 4, 4, S, (int)sa, S, (int)sb);
 }
 
-// LDS: STAGES steps of weights [CH][128] and rows [TOK][128], STAGES slots of
+// LDS: STAGES steps of weights [CH][128] and rows [TOK][128], kSlots slots of
 // scale words, then the tiles in front of each expert's.  A slot holds one
 // 16-byte word for every row of a step and the next, in the order of the
-// copies: of each wavefront's rows, then of its weight rows.  It is copied with
-// its first step; the word STAGES words before has its last step at least
-// STAGES steps before, which every wavefront has left by then.
+// copies: of each wavefront's rows, then of its weight rows.  With more than
+// two stages the words are copied one step later than the codes that they
+// belong to, STAGES - 2 steps ahead, which saves a slot (128 x 256 tiles have
+// room for three stages then).  The word kSlots words before has its last step
+// at least kSlots steps before, which every wavefront has left by then.
 template <int TOK, int CH, int NW, int STAGES>
 struct TiledLds {
   static constexpr int kW = CH / 8 / NW;                          // copies of weights a step
   static constexpr int kX = TOK / 8 / NW > 0 ? TOK / 8 / NW : 1;  // and of rows
   static constexpr int kStage = (TOK + CH) * 128;
   static constexpr int kScales = STAGES * kStage;
+  static constexpr bool kLate = STAGES > 2;
+  static constexpr int kSlots = kLate ? STAGES - 1 : STAGES;
   static constexpr int kWave8 = 8 * (kX + kW);  // words a wavefront copies
   static constexpr int kSlot = NW * 16 * kWave8;
-  static constexpr int kTable = kScales + STAGES * kSlot;
-  static constexpr int kBytes = kTable + 4 * (MOE_MAX_EXPERTS + 2);
+  static constexpr int kTable = kScales + kSlots * kSlot;
+  static constexpr int bytes(int n_experts) { return kTable + 4 * (n_experts + 1); }
   static_assert(kWave8 <= kWave && 32 % (8 * kX) == 0 && 32 % (8 * kW) == 0, "scale words");
 };
+constexpr int kMaxLds = 160 * 1024;
+
+// A copy of sixteen bytes a lane from base + voffset + soffset into LDS, as a
+// buffer load: the compiler counts it apart from the reads of LDS, where a
+// copy by a global pointer makes it wait for all of them at each one.
+__device__ __forceinline__ void copy_lds(const uint8_t* base, uint32_t bytes, uint32_t voffset,
+                                         uint32_t soffset, char* to) {
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)bytes,
+                                                   0x00020000);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16,
+                                           (int)voffset, (int)soffset, 0, 0);
+}
+
+// Exchanges between lanes that differ in one bit: the lower ones keep a and get
+// their partner's a for b, the upper ones keep b and get their partner's b for a.
+__device__ __forceinline__ void swap32(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap16(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+__device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
+  const uint32_t up = __builtin_amdgcn_update_dpp((int)a, (int)b, 0x128, 0xF, 0xC, false);
+  b = __builtin_amdgcn_update_dpp((int)b, (int)a, 0x128, 0xF, 0x3, false);
+  a = up;
+}
 
 // Large products: TOK rows x CH rows of weights (SwiGLU: gate and up of CH / 2
 // channels, sixteen of each a matrix instruction) a workgroup of WT x WC
@@ -350,46 +384,45 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   // Copies into LDS.  One copies 8 rows of 128 bytes; a lane's chunk is the
   // one that belongs at its place: chunk c of row r lies at c ^ (r / 2 % 8),
   // so that sixteen rows of an operand read meet different banks.
-  // Weights: a matrix of at most 2^31 bytes, an offset a lane.
-  const uint8_t* wbase[SWIGLU ? 2 : 1];  // of the item's expert, advanced by steps
-  uint32_t woffset[kW] = {};
+  constexpr int kMats = SWIGLU ? 2 : 1;
+  const uint32_t w_bytes = (uint32_t)p.rows * row_bytes;  // of a matrix, at most 2^31
+  const uint8_t *wbase[kMats], *wsbase[kMats];            // the item's expert; its words of scales
+  const uint8_t *xbase = p.x, *xsbase = p.x_scales;
+  uint32_t woffset[kW] = {}, xoffset[kX] = {}, wsoffset = 0, xsoffset = 0;
 #pragma unroll
-  for (int m = 0; m < (SWIGLU ? 2 : 1); ++m) wbase[m] = p.w[m];
-  const uint8_t* xsrc[kX];
-  const uint8_t* ssrc = nullptr;  // the scale word of lane: its rows' first, then its weights'
+  for (int m = 0; m < kMats; ++m) {
+    wbase[m] = p.w[m];
+    wsbase[m] = p.w_scales[m];
+  }
   const int chunk_even = (lane % 8) ^ (lane / 16);  // rows 8j + lane / 8 of even j
-  const bool scale_x = lane < 8 * kX;
-  const int64_t scale_step = (int64_t)(scale_x ? p.left_rows : p.rows) * 16;
   int load_step = 0, into = 0, scale_into = 0;
+  bool scales_due = false;
   auto x_copy = [&](int i) { return (wave * kX + i) % (TOK / 8); };
-  // LDS row r of the weights: its matrix and channel
-  auto weight_row = [&](int r, int j0, int& ch) {
-    if (!SWIGLU) {
-      ch = min(j0 + r, p.rows - 1);
-      return 0;
-    }
-    ch = min(j0 + r / 32 * 16 + r % 16, p.rows - 1);
-    return r / 16 % 2;
+  // the channel of LDS row r of the weights; of SwiGLU rows r / 16 % 2 are the up's
+  auto channel = [&](int r, int j0) {
+    return min(SWIGLU ? j0 + r / 32 * 16 + r % 16 : j0 + r, p.rows - 1);
   };
   auto open = [&]() {
     const Item it = find_item<TOK>(p, first, load_item, strips, kStripCh);
 #pragma unroll
-    for (int i = 0; i < kW; ++i) {
-      const int j = wave * kW + i;
-      const int chunk = chunk_even ^ (4 * (j & 1));
-      int ch;
-      weight_row(8 * j + lane / 8, it.j0, ch);
-      woffset[i] = (uint32_t)ch * row_bytes + 16 * chunk;
+    for (int m = 0; m < kMats; ++m) {
+      wbase[m] = p.w[m] + (int64_t)it.expert * w_bytes;
+      wsbase[m] = p.w_scales[m] + (int64_t)it.expert * p.words * p.rows * 16;
     }
 #pragma unroll
-    for (int m = 0; m < (SWIGLU ? 2 : 1); ++m)
-      wbase[m] = p.w[m] + (int64_t)it.expert * p.rows * row_bytes;
-    int scale_row = 0;
+    for (int i = 0; i < kW; ++i) {
+      const int j = wave * kW + i;
+      woffset[i] =
+          (uint32_t)channel(8 * j + lane / 8, it.j0) * row_bytes + 16 * (chunk_even ^ (4 * (j & 1)));
+    }
+    wsoffset = 16 * channel(wave * 8 * kW + lane % (SWIGLU ? 16 : 8 * kW), it.j0);
+    xsbase = p.x_scales;
+    if (p.top_k == 0) xbase = p.x + (int64_t)it.row0 * row_bytes;
 #pragma unroll
     for (int i = 0; i < kX; ++i) {
       const int j = x_copy(i);
-      const int chunk = chunk_even ^ (4 * (j & 1));
-      int row = it.row0 + min(8 * j + lane / 8, it.m - 1);
+      int row = min(8 * j + lane / 8, it.m - 1);
+      int scale_row = it.row0 + row;
       if (p.top_k != 0) {
         // through the scalar cache: a vector load's wait would drain the copies in flight
         const scalar_i32 perm = (scalar_i32)(uintptr_t)p.perm;
@@ -400,76 +433,73 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
           f = lane / 8 == r ? v : f;
         }
         row = f >= 0 && f < p.n_slots ? f / p.top_k : 0;
+        scale_row = row;
       }
-      xsrc[i] = p.x + (int64_t)row * row_bytes + 16 * chunk;
+      xoffset[i] = (uint32_t)row * row_bytes + 16 * (chunk_even ^ (4 * (j & 1)));
       // row 8i + r of this wavefront's is at lanes 8r .. 8r + 7
-      const int r = __shfl(row, 8 * (lane % 8));
-      scale_row = lane / 8 == i ? r : scale_row;
-    }
-    if (scale_x) {
-      ssrc = p.x_scales + (int64_t)scale_row * 16;
-    } else {
-      int ch;
-      const int r = wave * 8 * kW + min(lane - 8 * kX, 8 * kW - 1);
-      const uint8_t* ws = p.w_scales[0];
-      if (weight_row(r, it.j0, ch) != 0) ws = p.w_scales[1];
-      ssrc = ws + ((int64_t)it.expert * p.words * p.rows + ch) * 16;
+      const uint32_t r = 16 * __shfl(scale_row, 8 * (lane % 8));
+      xsoffset = i == 0 || lane / 8 == i ? r : xsoffset;
     }
   };
-  // the scale words of the next step and the one after it
+  // the scale words of a step and the one after it
   auto copy_scales = [&]() {
-    if (lane < L::kWave8)
-      __builtin_amdgcn_global_load_lds(
-          ssrc,
-          (__attribute__((address_space(3))) void*)(smem + L::kScales + scale_into * L::kSlot +
-                                                    wave * 16 * L::kWave8),
-          16, 0, 0);
-    ssrc += scale_step;
-    scale_into = scale_into + 1 == STAGES ? 0 : scale_into + 1;
+    char* const to = smem + L::kScales + scale_into * L::kSlot + wave * 16 * L::kWave8;
+    scale_into = scale_into + 1 == L::kSlots ? 0 : scale_into + 1;
+    if (lane < 8 * kX) copy_lds(xsbase, (uint32_t)p.left_rows * 16, xsoffset, 0, to);
+    if constexpr (SWIGLU && kW == 4) {
+      if (lane < 16)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          copy_lds(wsbase[m], (uint32_t)p.rows * 16, wsoffset, 0, to + 16 * (8 * kX + 16 * m));
+    } else {
+      if (lane < 8 * kW)
+        copy_lds(wsbase[SWIGLU ? wave * 8 * kW / 16 % 2 : 0], (uint32_t)p.rows * 16, wsoffset, 0,
+                 to + 16 * 8 * kX);
+    }
+    xsbase += (int64_t)p.left_rows * 16;
+#pragma unroll
+    for (int m = 0; m < kMats; ++m) wsbase[m] += (int64_t)p.rows * 16;
   };
-  // copy i of the next step into buffer b, and the step's end
+  // copy i of the next step into buffer b
   auto copy = [&](int i, int b) {
     const bool w = i < kW;
     const int j = w ? wave * kW + i : x_copy(i - kW);
-    const auto to = (__attribute__((address_space(3))) void*)(smem + b * L::kStage +
-                                                            ((w ? 0 : CH) + 8 * j) * 128);
-    if (w) {
-      // 16 rows of a matrix in turn
-      const uint8_t* const src = wbase[SWIGLU ? j / 2 % 2 : 0] + woffset[w ? i : 0];
-      __builtin_amdgcn_global_load_lds(src, to, 16, 0, 0);
-    } else {
-      const uint8_t*& src = xsrc[w ? 0 : i - kW];
-      __builtin_amdgcn_global_load_lds(src, to, 16, 0, 0);
-      src += 128;
-    }
+    char* const to = smem + b * L::kStage + ((w ? 0 : CH) + 8 * j) * 128;
+    if (w)  // 16 rows of a matrix in turn
+      copy_lds(wbase[SWIGLU ? j / 2 % 2 : 0], w_bytes, woffset[w ? i : 0], load_step * 128, to);
+    else
+      copy_lds(xbase, ~0u, xoffset[w ? 0 : i - kW], load_step * 128, to);
   };
   // What comes in front of a step's copies: a tile's first rows, the words of
-  // scales, and zeros of the rows instead of what lies past their end (the
-  // weights' first bytes of the step then, which zeros multiply).  Behind the last item
-  // the copies go on, with zeros and weights that nothing uses, so that every
-  // step has as many and no branch stands between its products.
+  // scales, and at a row's end the step's first bytes instead of what lies past
+  // it (any codes are finite, and the scales past the end, 2^-127 each, leave
+  // nothing of their products).  Behind the last item the copies go on, of
+  // bytes that nothing uses, so that every step has as many and no branch
+  // stands between its products.
   auto begin_step = [&]() {
-    const bool more = load_item < end;
-    if (more && load_step == 0) open();
-    if (more && load_step % 2 == 0) copy_scales();
-    if (more && load_step != tail) return;
+    if (L::kLate && scales_due) copy_scales();
+    scales_due = false;
+    if (load_item >= end) return;
+    if (load_step == 0) open();
+    if (load_step % 2 == 0) {
+      if (L::kLate)
+        scales_due = true;
+      else
+        copy_scales();
+    }
+    if (load_step != tail) return;
 #pragma unroll
     for (int i = 0; i < kW + kX; ++i) {
       const int j = i < kW ? wave * kW + i : x_copy(i - kW);
       const int chunk = chunk_even ^ (4 * (j & 1));
-      if (more && load_step * 128 + 16 * chunk < row_bytes) continue;
-      if (i < kW)
-        woffset[i < kW ? i : 0] -= more ? 16 * chunk : 0;
-      else
-        xsrc[i < kW ? 0 : i - kW] = reinterpret_cast<const uint8_t*>(&kZeroChunk);
+      if (load_step * 128 + 16 * chunk >= row_bytes)
+        (i < kW ? woffset[i < kW ? i : 0] : xoffset[i < kW ? 0 : i - kW]) -= 16 * chunk;
     }
   };
   // Without a branch: the compiler would move products past it.
   auto copied = [&]() {
     into = into + 1 == STAGES ? 0 : into + 1;
     const bool more = load_item < end, last = load_step + 1 == ksteps;
-#pragma unroll
-    for (int m = 0; m < (SWIGLU ? 2 : 1); ++m) wbase[m] += more && !last ? 128 : 0;
     load_step = more && !last ? load_step + 1 : 0;
     load_item += more && last ? per : 0;
   };
@@ -505,7 +535,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   auto read_x = [&](const char* buf, int u) {
     xv[u % 4] = *reinterpret_cast<const u32x4*>(buf + (xoff ^ (32 * (u / TB))) + u % TB * WT * 4096);
   };
-  int from = STAGES - 1, scale_from = STAGES - 1;
+  int from = STAGES - 1, scale_from = L::kSlots - 1;
   // the bytes of blocks 2h and 2h + 1 are 2h % 4 and 2h % 4 + 1 of the word's part h / 2; the
   // upper lanes take the second
   const char* scales = nullptr;
@@ -522,9 +552,12 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   // the next step's copies have landed, and every wavefront has read this
   // step's operands: the buffer is free
   auto next_step = [&](int step) {
+    // the compiler knows nothing of what the copies write: no read of LDS crosses here
+    asm volatile("" ::: "memory");
     step_barrier<(STAGES - 2) * kCopies>();
+    asm volatile("" ::: "memory");
     from = from + 1 == STAGES ? 0 : from + 1;
-    if (step % 2 == 0) scale_from = scale_from + 1 == STAGES ? 0 : scale_from + 1;
+    if (step % 2 == 0) scale_from = scale_from + 1 == L::kSlots ? 0 : scale_from + 1;
     const char* const buf = smem + from * L::kStage;
     scales = smem + L::kScales + scale_from * L::kSlot + step % 2 * 8;
     read_scales(0);
@@ -584,50 +617,66 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     // lane: token r32, channels 8q + 4 half .. + 3 of a block's quarter q; of
     // SwiGLU the gate's are quarters 0 and 1, the up's of the same channels 2 and 3
     constexpr int Q = SWIGLU ? 2 : 4;
+    constexpr int N = sizeof(O) == 2 ? 2 : 1;  // quarters in sixteen bytes
+    constexpr int kPieces = CB * Q / N;        // of sixteen bytes that a lane has of its token
+    constexpr int G = kPieces < 4 ? kPieces : 4;
 #pragma unroll
     for (int t = 0; t < TB; ++t) {
-      const int tok = (t * WT + wt) * 32 + r32;
-      O* const out = static_cast<O*>(p.out) + (it.row0 + (int64_t)tok) * p.out_stride;
-      // Two quarters' bf16 values change hands between the wavefront's halves,
-      // so that a lane stores 16 bytes.
-      constexpr int N = sizeof(O) == 2 ? 2 : 1;
+      uint32_t piece[kPieces][4];  // i: channels 4N (2i + half) .. + 4N - 1 of this wavefront's
 #pragma unroll
-      for (int c = 0; c < CB; ++c)
+      for (int i = 0; i < kPieces; ++i) {
+        const int c = i * N / Q, q = i * N % Q;
+        O v[4 * N];
 #pragma unroll
-        for (int q = 0; q < Q; q += N) {
-          struct alignas(16) {
-            O v[4 * N];
-          } o;
+        for (int k = 0; k < 4 * N; ++k)
+          v[k] = finish<SWIGLU, O>(acc[c][t][4 * q + k], acc[c][t][SWIGLU ? 8 + 4 * q + k : 0]);
+        __builtin_memcpy(piece[i], v, 16);
+        // two quarters' bf16 values change hands between the wavefront's halves
+        if (N == 2)
 #pragma unroll
-          for (int i = 0; i < 4 * N; ++i)
-            o.v[i] = finish<SWIGLU, O>(acc[c][t][4 * q + i], acc[c][t][SWIGLU ? 8 + 4 * q + i : 0]);
-          int j = it.j0 + (wc * CB + c) * 8 * Q + 8 * q + 4 * half;
-          if constexpr (N == 2) {
-            uint32_t w[4];
-            __builtin_memcpy(w, o.v, sizeof(w));
+          for (int k = 0; k < 2; ++k) swap32(piece[i][k], piece[i][2 + k]);
+      }
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const auto r = __builtin_amdgcn_permlane32_swap(w[i], w[2 + i], false, false);
-              w[i] = r[0];
-              w[2 + i] = r[1];
-            }
-            __builtin_memcpy(o.v, w, sizeof(w));
-            j += 4 * half;
-          }
+      for (int i = 0; i < kPieces; i += G) {
+        // G pieces of a lane change hands with the tokens 16 and 8 lanes on, so that a store
+        // writes 32 G whole bytes of each of its tokens (see the kernel's comment)
+        if constexpr (G >= 2)
+#pragma unroll
+          for (int k = 0; k < G / 2; ++k)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) swap16(piece[i + k][d], piece[i + k + G / 2][d]);
+        if constexpr (G == 4)
+#pragma unroll
+          for (int k = 0; k < 4; k += 2)
+#pragma unroll
+            for (int d = 0; d < 4; ++d) swap8(piece[i + k][d], piece[i + k + 1][d]);
+#pragma unroll
+        for (int k = 0; k < G; ++k) {
+          const int local = G == 4 ? r32 % 8 + 8 * (k % 2) + 16 * (k / 2)
+                            : G == 2 ? r32 % 16 + 16 * k
+                                     : r32;
+          const int mine = G == 4 ? r32 / 16 * 2 + r32 / 8 % 2 : G == 2 ? r32 / 16 : 0;
+          const int tok = (t * WT + wt) * 32 + local;
+          const int j = it.j0 + wc * CB * 8 * Q + 4 * N * (2 * (i + mine) + half);
+          O* const out = static_cast<O*>(p.out) + (it.row0 + (int64_t)tok) * p.out_stride + j;
           if (tok >= it.m) continue;
           if (j + 4 * N <= p.rows) {
             // grouped outputs past the caches, which the weights go through
             if (past)
-              __builtin_nontemporal_store(__builtin_bit_cast(u32x4, o),
-                                          reinterpret_cast<u32x4*>(out + j));
+              __builtin_nontemporal_store(
+                  u32x4{piece[i + k][0], piece[i + k][1], piece[i + k][2], piece[i + k][3]},
+                  reinterpret_cast<u32x4*>(out));
             else
-              __builtin_memcpy(out + j, o.v, 16);
+              __builtin_memcpy(out, piece[i + k], 16);
           } else {
+            O v[4 * N];
+            __builtin_memcpy(v, piece[i + k], 16);
 #pragma unroll
-            for (int i = 0; i < 4 * N; ++i)
-              if (j + i < p.rows) out[j + i] = o.v[i];
+            for (int d = 0; d < 4 * N; ++d)
+              if (j + d < p.rows) out[d] = v[d];
           }
         }
+      }
     }
   }
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy outlives the workgroup's LDS
@@ -645,12 +694,13 @@ constexpr TiledShape kTiled[kDirect32] = {{256, 256, 1}, {128, 256, 1}, {64, 256
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) {
   using L = TiledLds<TOK, CH, WT * WC, STAGES>;
-  static_assert(L::kBytes <= 160 * 1024, "LDS");
+  static_assert(L::bytes(1) <= kMaxLds, "LDS");
   constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
   static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
+      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
   if (attr != hipSuccess) return attr;
-  hipLaunchKernelGGL(kernel, dim3(kCus * per_cu), dim3(kWave * WT * WC), L::kBytes, stream, p);
+  hipLaunchKernelGGL(kernel, dim3(kCus * per_cu), dim3(kWave * WT * WC), L::bytes(p.n_experts),
+                     stream, p);
   return hipGetLastError();
 }
 
@@ -680,11 +730,11 @@ hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
   const Form f = choose_form(p, SWIGLU);
   switch (f) {
     case k256x256: return launch_tiled<SWIGLU, O, 256, 256, 2, 4, 2>(p, 1, stream);
-    case k128x256: return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 2>(p, 1, stream);
+    case k128x256: return launch_tiled<SWIGLU, O, 128, 256, 2, 4, 3>(p, 1, stream);
     case k64x256: return launch_tiled<SWIGLU, O, 64, 256, 2, 4, 3>(p, 1, stream);
     case k32x256: return launch_tiled<SWIGLU, O, 32, 256, 1, 8, 3>(p, 1, stream);
     case k128x128: return launch_tiled<SWIGLU, O, 128, 128, 2, 4, 4>(p, 1, stream);
-    case k64x64: return launch_tiled<SWIGLU, O, 64, 64, 2, 2, 3>(p, 2, stream);
+    case k64x64: return launch_tiled<SWIGLU, O, 64, 64, 2, 2, 4>(p, 2, stream);
     case kDirect32: launch_direct<SWIGLU, O, 2, SWIGLU ? 1 : 2>(p, stream); break;
     default: launch_direct<SWIGLU, O, 1, 1>(p, stream);
   }
