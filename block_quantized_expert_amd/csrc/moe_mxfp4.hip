@@ -147,7 +147,6 @@ __device__ __forceinline__ f32x4 mfma_fp4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa
 }
 
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));  // scale bytes of 256 inputs
-typedef uint32_t u32x1 __attribute__((ext_vector_type(1)));
 
 // Small products: 16 TB rows x 16 CB channels a workgroup (SwiGLU: CB 1, gate
 // and up), the reduction dealt to the wavefronts in turns of 256 inputs,
@@ -312,12 +311,14 @@ constexpr int kMaxLds = 160 * 1024;
 // A copy of sixteen bytes a lane from base + voffset + soffset into LDS, as a
 // buffer load: the compiler counts it apart from the reads of LDS, where a
 // copy by a global pointer makes it wait for all of them at each one.
+// PAST: past the caches.
+template <bool PAST = false>
 __device__ __forceinline__ void copy_lds(const uint8_t* base, uint32_t bytes, uint32_t voffset,
                                          uint32_t soffset, char* to) {
   const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(base), 0, (int)bytes,
                                                    0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16,
-                                           (int)voffset, (int)soffset, 0, 0);
+                                           (int)voffset, (int)soffset, 0, PAST ? 2 : 0);
 }
 
 // Exchanges between lanes that differ in one bit: the lower ones keep a and get
@@ -397,6 +398,9 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   const int chunk_even = (lane % 8) ^ (lane / 16);  // rows 8j + lane / 8 of even j
   int load_step = 0, into = 0, scale_into = 0;
   bool scales_due = false;
+  // an expert's only tile, whose weights are read once
+  constexpr bool kOnce = TB == 1 && CH == 256;
+  bool load_only = false;
   auto x_copy = [&](int i) { return (wave * kX + i) % (TOK / 8); };
   // the channel of LDS row r of the weights; of SwiGLU rows r / 16 % 2 are the up's
   auto channel = [&](int r, int j0) {
@@ -404,6 +408,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   };
   auto open = [&]() {
     const Item it = find_item<TOK>(p, first, load_item, strips, kStripCh);
+    load_only = it.only;
 #pragma unroll
     for (int m = 0; m < kMats; ++m) {
       wbase[m] = p.w[m] + (int64_t)it.expert * w_bytes;
@@ -461,12 +466,13 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     for (int m = 0; m < kMats; ++m) wsbase[m] += (int64_t)p.rows * 16;
   };
   // copy i of the next step into buffer b
-  auto copy = [&](int i, int b) {
+  auto copy = [&](int i, int b, auto once) {
     const bool w = i < kW;
     const int j = w ? wave * kW + i : x_copy(i - kW);
     char* const to = smem + b * L::kStage + ((w ? 0 : CH) + 8 * j) * 128;
     if (w)  // 16 rows of a matrix in turn
-      copy_lds(wbase[SWIGLU ? j / 2 % 2 : 0], w_bytes, woffset[w ? i : 0], load_step * 128, to);
+      copy_lds<decltype(once)::value>(wbase[SWIGLU ? j / 2 % 2 : 0], w_bytes, woffset[w ? i : 0],
+                                      load_step * 128, to);
     else
       copy_lds(xbase, ~0u, xoffset[w ? 0 : i - kW], load_step * 128, to);
   };
@@ -507,11 +513,11 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   for (int i = 0; i < STAGES - 1; ++i) {
     begin_step();
 #pragma unroll
-    for (int c = 0; c < kW + kX; ++c) copy(c, into);
+    for (int c = 0; c < kW + kX; ++c) copy(c, into, std::false_type());
     copied();
   }
 
-  const int swz = 16 * (half ^ (r32 / 2 % 8));
+  const int swz = 16 * (4 * half ^ (r32 / 2 % 8));  // chunks 0 to 3 of a row, and 4 to 7
   const int woff = (wc * CB * 32 + r32) * 128 + swz;
   const int xoff = (CH + wt * 32 + r32) * 128 + swz;  // its blocks of rows: every WT-th
   auto scale_at = [&](int r, int each, int at) {
@@ -526,29 +532,17 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   constexpr int kWRing = TB > 1 ? 2 : 4;
   constexpr int kCopies = kW + kX;
   u32x4 wv[kWRing][CB], xv[4];
-  uint32_t ws[2][CB], xs[2][TB];  // scale bytes of the step's first and second 128 inputs
+  uint32_t ws[CB], xs[TB];     // the scale bytes of a lane's four chunks
+  u32x2 wnext[CB], xnext[TB];  // the next step's, of both halves' chunks
   auto read_w = [&](const char* buf, int h) {
 #pragma unroll
     for (int c = 0; c < CB; ++c)
-      wv[h % kWRing][c] = *reinterpret_cast<const u32x4*>(buf + (woff ^ (32 * h)) + c * 4096);
+      wv[h % kWRing][c] = *reinterpret_cast<const u32x4*>(buf + (woff ^ (16 * h)) + c * 4096);
   };
   auto read_x = [&](const char* buf, int u) {
-    xv[u % 4] = *reinterpret_cast<const u32x4*>(buf + (xoff ^ (32 * (u / TB))) + u % TB * WT * 4096);
+    xv[u % 4] = *reinterpret_cast<const u32x4*>(buf + (xoff ^ (16 * (u / TB))) + u % TB * WT * 4096);
   };
   int from = STAGES - 1, scale_from = L::kSlots - 1;
-  // the bytes of blocks 2h and 2h + 1 are 2h % 4 and 2h % 4 + 1 of the word's part h / 2; the
-  // upper lanes take the second
-  const char* scales = nullptr;
-  auto read_scales = [&](int d) {
-#pragma unroll
-    for (int c = 0; c < CB; ++c)
-      ws[d][c] = (*reinterpret_cast<const u32x1*>(scales + wscale + 4 * d +
-                                                  c * 32 / (8 * kW) * L::kWave8 * 16))[0];
-#pragma unroll
-    for (int t = 0; t < TB; ++t)
-      xs[d][t] = (*reinterpret_cast<const u32x1*>(scales + xscale + 4 * d +
-                                                  t * WT * 32 / (8 * kX) * L::kWave8 * 16))[0];
-  };
   // the next step's copies have landed, and every wavefront has read this
   // step's operands: the buffer is free
   auto next_step = [&](int step) {
@@ -559,15 +553,23 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     from = from + 1 == STAGES ? 0 : from + 1;
     if (step % 2 == 0) scale_from = scale_from + 1 == L::kSlots ? 0 : scale_from + 1;
     const char* const buf = smem + from * L::kStage;
-    scales = smem + L::kScales + scale_from * L::kSlot + step % 2 * 8;
-    read_scales(0);
+    // eight bytes a lane: reads of four would meet on a quarter of the banks (8 cycles each, these 4)
+    const char* const scales = smem + L::kScales + scale_from * L::kSlot + step % 2 * 8;
+#pragma unroll
+    for (int c = 0; c < CB; ++c)
+      wnext[c] = *reinterpret_cast<const u32x2*>(scales + wscale +
+                                                 c * 32 / (8 * kW) * L::kWave8 * 16);
+#pragma unroll
+    for (int t = 0; t < TB; ++t)
+      xnext[t] = *reinterpret_cast<const u32x2*>(scales + xscale +
+                                                 t * WT * 32 / (8 * kX) * L::kWave8 * 16);
     read_w(buf, 0);
     read_x(buf, 0);
     read_x(buf, 1);
     if (TB == 1) read_w(buf, 1);
   };
   next_step(0);
-  const bool past = grouped && reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
+  const bool past = reinterpret_cast<uintptr_t>(p.out) % 16 == 0 &&
                     p.out_stride * sizeof(O) % 16 == 0;
   for (; item < end; item += per) {
     const Item it = find_item<TOK>(p, first, item, strips, kStripCh);
@@ -578,10 +580,12 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
       for (int t = 0; t < TB; ++t)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[c][t][i] = 0.0f;
-    for (int ks = 0; ks < ksteps; ++ks) {
-      begin_step();
+    auto step = [&](int next, auto once) {
       const char* const buf = smem + from * L::kStage;
-      read_scales(1);
+#pragma unroll
+      for (int c = 0; c < CB; ++c) ws[c] = half != 0 ? wnext[c][1] : wnext[c][0];
+#pragma unroll
+      for (int t = 0; t < TB; ++t) xs[t] = half != 0 ? xnext[t][1] : xnext[t][0];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int h = u / TB, t = u % TB;
@@ -593,26 +597,31 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
         constexpr int kSpan = STAGES == 2 ? U / 2 : U - 2;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i)
-          if (i * kSpan / kCopies == u) copy(i, into);
+          if (i * kSpan / kCopies == u) copy(i, into, once);
         if (u == U - 2) {
           copied();
-          next_step(ks + 1 == ksteps ? 0 : ks + 1);
+          next_step(next);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (h % 2 == 0) {
-          if (t == 0)
 #pragma unroll
-            for (int c = 0; c < CB; ++c) ws[h / 2][c] >>= 8 * half;
-          xs[h / 2][t] >>= 8 * half;
+        for (int c = 0; c < CB; ++c) {
+          const u32x4 wf = wv[h % kWRing][c], xf = xv[u % 4];
+          f32x16& d = acc[c][t];
+          d = h == 0   ? mfma_fp4_32<0>(wf, xf, d, ws[c], xs[t])
+              : h == 1 ? mfma_fp4_32<1>(wf, xf, d, ws[c], xs[t])
+              : h == 2 ? mfma_fp4_32<2>(wf, xf, d, ws[c], xs[t])
+                       : mfma_fp4_32<3>(wf, xf, d, ws[c], xs[t]);
         }
-#pragma unroll
-        for (int c = 0; c < CB; ++c)
-          acc[c][t] = h % 2 == 0 ? mfma_fp4_32<0>(wv[h % kWRing][c], xv[u % 4], acc[c][t],
-                                                  ws[h / 2][c], xs[h / 2][t])
-                                 : mfma_fp4_32<2>(wv[h % kWRing][c], xv[u % 4], acc[c][t],
-                                                  ws[h / 2][c], xs[h / 2][t]);
         __builtin_amdgcn_sched_barrier(0);
       }
+    };
+    for (int ks = 0; ks < ksteps; ++ks) {
+      begin_step();
+      const int next = ks + 1 == ksteps ? 0 : ks + 1;
+      if (kOnce && load_only)
+        step(next, std::true_type());
+      else
+        step(next, std::false_type());
     }
     // lane: token r32, channels 8q + 4 half .. + 3 of a block's quarter q; of
     // SwiGLU the gate's are quarters 0 and 1, the up's of the same channels 2 and 3
