@@ -123,18 +123,16 @@ constexpr int kCus = 256;
 template <int TOK>
 __device__ __forceinline__ void tile_table(const GroupedRows& p, int32_t* first) {
   const int lane = threadIdx.x % kWave;
-  const bool grouped = p.offsets != nullptr;
-  const int n_exp = grouped ? p.n_experts : 1;
-  int off[kTableSpan + 1], sum = 0;
-  if (grouped) {
-#pragma unroll
-    for (int i = 0; i <= kTableSpan; ++i) off[i] = p.offsets[min(lane * kTableSpan + i, n_exp)];
-#pragma unroll
-    for (int i = 0; i <= kTableSpan; ++i) off[i] = min(max(off[i], 0), p.n_slots);
-  } else {
-#pragma unroll
-    for (int i = 0; i <= kTableSpan; ++i) off[i] = lane + i == 0 ? 0 : p.n_slots;
+  if (p.offsets == nullptr) {
+    if (lane < 2) first[lane] = lane * ((p.n_slots + TOK - 1) / TOK);
+    return;
   }
+  const int n_exp = p.n_experts;
+  int off[kTableSpan + 1], sum = 0;
+#pragma unroll
+  for (int i = 0; i <= kTableSpan; ++i) off[i] = p.offsets[min(lane * kTableSpan + i, n_exp)];
+#pragma unroll
+  for (int i = 0; i <= kTableSpan; ++i) off[i] = min(max(off[i], 0), p.n_slots);
 #pragma unroll
   for (int i = 0; i < kTableSpan; ++i) sum += (max(off[i + 1] - off[i], 0) + TOK - 1) / TOK;
   int incl = sum;

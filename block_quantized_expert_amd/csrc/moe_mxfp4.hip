@@ -691,19 +691,27 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): no copy outlives the workgroup's LDS
 }
 
-// The kernels' forms.
+// The kernels' forms, and what a product takes with each, in microseconds:
+// least squares on the logarithms of every form's times over dense and grouped
+// products of 1 to 24576 rows, without the rounding of the left operand.  To be
+// fitted anew when a form's kernel changes.
 enum Form { k256x256, k128x256, k64x256, k32x256, k128x128, k64x64, kDirect32, kDirect16 };
-struct TiledShape {
-  int rows, ch;  // tile (SwiGLU: of ch / 2 channels)
-  int per_cu;    // workgroups on a CU
+struct TiledCost {
+  int rows, ch;             // tile (SwiGLU: of ch / 2 channels)
+  int per_cu;               // workgroups on a CU
+  double start;             // the launch, the first loads, the last stores
+  double step, cold, tile;  // a tile's time for each step of 256 inputs, more
+                            // of it where the weights come from HBM, and once
 };
-constexpr TiledShape kTiled[kDirect32] = {{256, 256, 1}, {128, 256, 1}, {64, 256, 1},
-                                          {32, 256, 1},  {128, 128, 1}, {64, 64, 2}};
+constexpr TiledCost kTiledCost[kDirect32] = {
+    {256, 256, 1, 9.8, 1.63, 0.86, 0.9}, {128, 256, 1, 6.4, 0.99, 0.39, 1.8},
+    {64, 256, 1, 4.8, 0.78, 0.33, 2.1},  {32, 256, 1, 4.6, 0.67, 0.40, 1.8},
+    {128, 128, 1, 6.1, 0.64, 0.16, 1.0}, {64, 64, 2, 4.4, 0.43, 0.23, 1.6}};
 
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) {
   using L = TiledLds<TOK, CH, WT * WC, STAGES>;
-  static_assert(L::bytes(1) <= kMaxLds, "LDS");
+  static_assert(L::bytes(MOE_MAX_EXPERTS) <= kMaxLds || (TOK == 128 && CH == 256), "LDS");
   constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
   static const hipError_t attr = hipFuncSetAttribute(
       reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
@@ -714,12 +722,48 @@ hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) 
 }
 
 Form choose_form(const ProductParams& p, bool swiglu) {
+  const int steps = (p.cols + 255) / 256;
+  const double live = p.n_slots < p.n_experts ? p.n_slots : p.n_experts;
+  const double row_bytes = p.cols * 17.0 / 32;
+  // weights past the 256 MB memory-side cache
+  const bool cold = live * p.rows * row_bytes * (swiglu ? 2 : 1) > 256e6;
   const double mean = (double)p.n_slots / p.n_experts;
-  if (mean <= 16 || p.n_slots <= 32) return kDirect16;
-  if (mean <= 32) return k32x256;
-  if (mean <= 64) return k64x256;
-  if (mean <= 128) return k128x256;
-  return k256x256;
+  Form best = kDirect16;
+  double least = 0;
+  // The direct forms: the launch and the look-up of a tile, the latency of a
+  // reduction by its length, both operands' bytes (every workgroup reads its
+  // own) at a rate of L2 that weights from HBM divide by about two, and a
+  // workgroup's start.
+  for (int wide = 0; wide < 2; ++wide) {
+    const int tm = wide ? 32 : 16, strip = wide && !swiglu ? 32 : 16;
+    const double groups = expected_tiles(p, tm) * ((p.rows + strip - 1) / strip);
+    const double bytes = groups * row_bytes * ((swiglu ? 32 : strip) + (mean < tm ? mean : tm));
+    const double us = wide ? 3.1 + p.cols * 0.36e-3 + bytes * (cold ? 1.86 : 1) / 9.6e6 + groups * 4.1e-3
+                           : 2.9 + bytes * (cold ? 1.66 : 1) / 9.9e6 + groups * 2.1e-3;
+    if (!wide || us < least) {
+      best = wide ? kDirect32 : kDirect16;
+      least = us;
+    }
+  }
+  // a copy's 32-bit offset reaches 4 GiB of rows that are gathered
+  if (p.top_k > 0 && (int64_t)p.left_rows * (p.cols / 2) > UINT32_MAX) return best;
+  for (int f = 0; f < kDirect32; ++f) {
+    const TiledCost& c = kTiledCost[f];
+    // the one form whose table of the most experts passes the CU's LDS
+    if (f == k128x256 && TiledLds<128, 256, 8, 3>::bytes(p.n_experts) > kMaxLds) continue;
+    const int strip = swiglu ? c.ch / 2 : c.ch;
+    const double items = expected_tiles(p, c.rows) * ((p.rows + strip - 1) / strip);
+    // a dense product's tiles are known, its last round costs like a whole one;
+    // grouped, the tiles' heights differ and even the last round out to 0.3
+    double rounds = items / (kCus * c.per_cu);
+    rounds = p.offsets == nullptr ? ceil(rounds) : rounds > 1 ? rounds + 0.3 : 1.0;
+    const double us = c.start + rounds * (steps * (c.step + (cold ? c.cold : 0)) + c.tile);
+    if (us < least) {
+      best = (Form)f;
+      least = us;
+    }
+  }
+  return best;
 }
 
 template <bool SWIGLU, typename O, int TB, int CB>
