@@ -70,79 +70,283 @@ __device__ __forceinline__ double wave_sum(double v) {
 }
 
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-  for (int s = kWave / 2; s > 0; s >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, s));
-  return v;
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x128, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x124, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x122, 0xF, 0xF, true));
+  v = max(v, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x121, 0xF, 0xF, true));
+  const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+  v = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+  return max(b[0], b[1]);
 }
 
+// Eight weights as stored: sixteen bytes twice, of bf16 the same ones.  No
+// branch: one in front of loads would make each wait for the last.
 struct Weight8 {
   u32x4 lo, hi;
   __device__ float at(int i, int bf16) const {
-    const uint32_t b = bf16 ? (i & 1 ? lo[i / 2] & 0xFFFF0000u : lo[i / 2] << 16)
-                            : (i < 4 ? lo[i] : hi[i - 4]);
-    return __uint_as_float(b);
+    const uint32_t half = i & 1 ? lo[i / 2] & 0xFFFF0000u : lo[i / 2] << 16;
+    return __uint_as_float(bf16 ? half : i < 4 ? lo[i] : hi[i - 4]);
   }
 };
-// Eight weights as stored; the branches are the same for the whole launch.
-__device__ __forceinline__ Weight8 load_weight(const NormParams& p, int c, int m) {
-  Weight8 r{};
-  if (m < 8) {
-    Cols8<__bf16> b{};
-    Cols8<float> f{};
-    if (p.w_bf16)
-      b = load_cols(static_cast<const __bf16*>(p.weight) + c, m);
-    else
-      f = load_cols(static_cast<const float*>(p.weight) + c, m);
-    if (p.w_bf16)
-      __builtin_memcpy(&r.lo, &b, 16);
-    else
-      __builtin_memcpy(&r, &f, 32);
-  } else if (p.w_bf16) {
-    __builtin_memcpy(&r.lo, static_cast<const __bf16*>(p.weight) + c, 16);
-  } else {
-    __builtin_memcpy(&r, static_cast<const float*>(p.weight) + c, 32);
-  }
+__device__ __forceinline__ Weight8 load_weight(const void* weight, int bf16, int c) {
+  Weight8 r;
+  const char* const at = static_cast<const char*>(weight) + (int64_t)c * (bf16 ? 2 : 4);
+  __builtin_memcpy(&r.lo, at, 16);
+  __builtin_memcpy(&r.hi, at + (bf16 ? 0 : 16), 16);
   return r;
 }
+// At the end of a row of any length.
+__device__ __forceinline__ float weight_at(const void* weight, int bf16, int c) {
+  return bf16 ? static_cast<float>(static_cast<const __bf16*>(weight)[c])
+              : static_cast<const float*>(weight)[c];
+}
 
-// W wavefronts a row, eight columns a lane; rows of one wavefront share a
-// workgroup by fours.  LONG: longer rows, whose columns past the first 8192
-// are read again once the sum is known.
-template <typename X, typename S, bool RES, typename O, int W, bool LONG>
-__global__ __launch_bounds__(kWave*(W < 4 ? 4 : W)) void rmsnorm_kernel(NormParams p) {
-  constexpr int kRows = W < 4 ? 4 / W : 1;
+// Eight columns past the caches.  Of many rows the stores go there: lines that
+// stay would cost other lines' write-back (4096 x 4096 bf16, the residual added:
+// 31.3 us, y past the caches 28.8, the total as well 22.8; loads there 25.3;
+// gradients 30.5, dx past them 24.7).
+typedef uint32_t PastVec __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T>
+__device__ __forceinline__ void store_past(T* p, const Cols8<T>& r) {
+  PastVec v[sizeof(r) / 16];
+  __builtin_memcpy(v, &r, sizeof(r));
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r) / 16; ++i)
+    __builtin_nontemporal_store(v[i], reinterpret_cast<PastVec*>(p) + i);
+}
+
+// Where a lane's eight columns lie that begin at `nominal`: rows have at least
+// eight columns, and the last lane takes the last eight, of which the first
+// `skip` belong to its neighbour; a lane past the row's end skips all of them.
+// So every lane loads without a branch.
+struct Columns {
+  int c, skip;
+  __device__ Columns(int nominal, int hidden)
+      : c(nominal + 8 <= hidden ? nominal : hidden - 8),
+        skip(nominal + 8 <= hidden ? 0 : nominal < hidden ? nominal + 8 - hidden : 8) {}
+};
+template <bool PAST, typename T>
+__device__ __forceinline__ void store_own(T* row, const Columns& at, const Cols8<T>& r) {
+  if (at.skip == 0) {
+    if (PAST)
+      store_past(row + at.c, r);
+    else
+      __builtin_memcpy(row + at.c, &r, sizeof(r));
+  } else if (at.skip < 8) {
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i >= at.skip) row[at.c + i] = r.v[i];
+  }
+}
+
+// A row's eight rounded values: codes and the scale byte of each block.  Every
+// lane of the wavefront calls this; its columns are one word of scales, the
+// word's padding included.
+template <bool PAST>
+__device__ __forceinline__ void store_mxfp4(const NormParams& p, int64_t row, int c,
+                                            const float (&n)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, magnitude(n[i]));
+  const uint32_t byte = mxfp4_byte(block_max(m));
+  if (c / 512 * 512 < p.hidden && threadIdx.x % 4 == 0)
+    static_cast<uint8_t*>(p.scale)[((c / 512) * p.n_rows + row) * 16 + c / 32 % 16] =
+        c < p.hidden ? byte : 0;
+  if (c < p.hidden) {
+    const uint32_t codes = mxfp4_codes(n, byte);
+    auto* const to =
+        reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * (p.hidden / 2) + c / 2);
+    if (PAST)
+      __builtin_nontemporal_store(codes, to);
+    else
+      *to = codes;
+  }
+}
+template <bool PAST>
+__device__ __forceinline__ void store_int8(const NormParams& p, int64_t row, int c,
+                                           const float (&n)[8], uint32_t top) {
+  const float a = __uint_as_float(top), inv = 127.0f / a;
+  uint32_t o[2] = {0, 0};
+  if (top < 0x7F800000u && top != 0) {
+    // quantized() of each, with one branch for all eight: most wavefronts have no value at a border
+    float q[8];
+    bool border = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float r = n[i] * inv;
+      q[i] = rintf(r);
+      border |= !(fabsf(fabsf(r - q[i]) - 0.5f) > 0x1p-14f);
+    }
+    if (border)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) q[i] = (float)quantized(n[i], a, inv);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i / 4] |= (uint32_t)((int)q[i] & 0xFF) << (8 * (i % 4));
+  }
+  typedef uint32_t Word2 __attribute__((ext_vector_type(2)));
+  auto* const to = reinterpret_cast<Word2*>(static_cast<int8_t*>(p.y) + row * p.hidden + c);
+  if (PAST)
+    __builtin_nontemporal_store(Word2{o[0], o[1]}, to);
+  else
+    *to = Word2{o[0], o[1]};
+}
+__device__ __forceinline__ float int8_scale(uint32_t top) {
+  return top < 0x7F800000u ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7FC00000u);
+}
+
+// W wavefronts a row, V times eight columns a lane, in registers; rows of one
+// wavefront share a workgroup by fours.  A workgroup takes every gridDim.x-th
+// row (or four), with the weights in registers.
+template <typename X, typename S, bool RES, typename O, int W, int V>
+__global__ __launch_bounds__(kWave*(W == 1 ? 4 : W)) void rmsnorm_kernel(NormParams p) {
+  constexpr int kRows = W == 1 ? 4 : 1;
   constexpr int kSpan = W * kWave * 8;
+  constexpr bool kPast = V > 1;  // many rows: what is written goes past the caches
+  constexpr bool kInt8 = std::is_same<O, Int8>::value, kMx = std::is_same<O, Mxfp4>::value;
+  constexpr bool kBf16 = std::is_same<O, __bf16>::value;
+  __shared__ double part[2][W];
+  __shared__ uint32_t part_top[2][W];
+  const int t = threadIdx.x % (W * kWave), wave = t / kWave;
+  Cols8<X> ahead_x[V];
+  Cols8<S> ahead_res[V];
+  auto load = [&](int64_t row) {
+    if (row >= p.n_rows) return;  // the same for a row's wavefronts
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = Columns(8 * t + v * kSpan, p.hidden).c;
+      ahead_x[v] = load_cols(static_cast<const X*>(p.x) + row * p.x_stride + c);
+      if constexpr (RES)
+        ahead_res[v] = load_cols(static_cast<const S*>(p.residual) + row * p.res_stride + c);
+    }
+  };
+  int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / (W * kWave);
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  load(row);
+  float w[V][8];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const Weight8 wv = load_weight(p.weight, p.w_bf16, Columns(8 * t + v * kSpan, p.hidden).c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[v][i] = wv.at(i, p.w_bf16);
+  }
+  int turn = 0;
+  for (; row < p.n_rows; row += step, turn ^= 1) {
+    S* const total = RES ? static_cast<S*>(p.total) + row * p.total_stride : nullptr;
+    Cols8<X> a[V];
+    Cols8<S> b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      a[v] = ahead_x[v];
+      if constexpr (RES) b[v] = ahead_res[v];
+    }
+    load(row + step);
+    float s[V][8];
+    double sum = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const Columns at(8 * t + v * kSpan, p.hidden);
+      if constexpr (RES) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          b[v].v[i] = static_cast<S>(static_cast<float>(a[v].v[i]) + static_cast<float>(b[v].v[i]));
+        store_own<kPast>(total, at, b[v]);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float si = RES ? static_cast<float>(b[v].v[i]) : static_cast<float>(a[v].v[i]);
+        s[v][i] = i < at.skip ? 0.0f : si;
+        sum = fma((double)s[v][i], (double)s[v][i], sum);
+      }
+    }
+    sum = wave_sum(sum);
+    if (W > 1) {
+      if (t % kWave == 0) part[turn][wave] = sum;
+      __syncthreads();
+      sum = 0;
+#pragma unroll
+      for (int i = 0; i < W; ++i) sum += part[turn][i];
+    }
+    const double r = rsqrt(sum * p.inv_hidden + p.eps);
+    const float rf = (float)r;
+    uint32_t top = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[v][i] = kBf16 ? s[v][i] * rf * w[v][i] : (float)((double)s[v][i] * r * (double)w[v][i]);
+        if (kInt8) top = max(top, magnitude(s[v][i]));
+      }
+    if (kInt8) {  // a row's own scale; lanes past the row's end hold 0, or NaN with the row
+      top = wave_max(top);
+      if (W > 1) {
+        if (t % kWave == 0) part_top[turn][wave] = top;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < W; ++i) top = max(top, part_top[turn][i]);
+      }
+      if (t == 0) static_cast<float*>(p.scale)[row] = int8_scale(top);
+    }
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = 8 * t + v * kSpan;
+      if constexpr (kMx) {
+        store_mxfp4<kPast>(p, row, c, s[v]);
+      } else if constexpr (kInt8) {
+        if (c < p.hidden) store_int8<kPast>(p, row, c, s[v], top);
+      } else {
+        Cols8<O> o;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o.v[i] = static_cast<O>(s[v][i]);
+        store_own<kPast>(static_cast<O*>(p.y) + row * p.y_stride, Columns(c, p.hidden), o);
+      }
+    }
+  }
+}
+
+// Rows of more than 8192 columns, or fewer than eight: a workgroup a row, its
+// columns read again once the sum is known.
+template <typename X, typename S, bool RES, typename O>
+__global__ __launch_bounds__(16 * kWave) void rmsnorm_long_kernel(NormParams p) {
+  constexpr int W = 16, kSpan = W * kWave * 8;
   constexpr bool kInt8 = std::is_same<O, Int8>::value, kMx = std::is_same<O, Mxfp4>::value;
   constexpr bool kBf16 = std::is_same<O, __bf16>::value;
   __shared__ double part[W];
   __shared__ uint32_t part_top[W];
-  const int t = threadIdx.x % (W * kWave), wave = t / kWave;
-  const int64_t row = p.row0 + (int64_t)blockIdx.x * kRows + threadIdx.x / (W * kWave);
-  if (row >= p.n_rows) return;  // whole wavefronts, and only where no barrier follows
+  const int64_t row = p.row0 + blockIdx.x;
   const X* const x = static_cast<const X*>(p.x) + row * p.x_stride;
   const S* const res = RES ? static_cast<const S*>(p.residual) + row * p.res_stride : nullptr;
   S* const total = RES ? static_cast<S*>(p.total) + row * p.total_stride : nullptr;
-
-  // s of columns c .. c + 7, which is written to total
-  auto open = [&](int c, float (&s)[8]) {
+  double sum = 0;
+  for (int c = 8 * threadIdx.x; c < p.hidden; c += kSpan) {
     const int m = p.hidden - c;
     const Cols8<X> a = load_cols(x + c, m);
-    if constexpr (RES) {
-      const Cols8<S> b = load_cols(static_cast<const S*>(res) + c, m);
-      Cols8<S> sum;
+    Cols8<S> b{};
+    if constexpr (RES) b = load_cols(res + c, m);
+    float s[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        sum.v[i] = static_cast<S>(static_cast<float>(a.v[i]) + static_cast<float>(b.v[i]));
-        s[i] = static_cast<float>(sum.v[i]);
+    for (int i = 0; i < 8; ++i) {
+      s[i] = static_cast<float>(a.v[i]);
+      if constexpr (RES) {
+        b.v[i] = static_cast<S>(s[i] + static_cast<float>(b.v[i]));
+        s[i] = static_cast<float>(b.v[i]);
       }
-      store_cols(total + c, sum, m);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) s[i] = static_cast<float>(a.v[i]);
+      sum = fma((double)s[i], (double)s[i], sum);
     }
-  };
-  auto again = [&](int c, float (&s)[8]) {
+    if constexpr (RES) store_cols(total + c, b, m);
+  }
+  sum = wave_sum(sum);
+  if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = sum;
+  __syncthreads();
+  sum = 0;
+#pragma unroll
+  for (int i = 0; i < W; ++i) sum += part[i];
+  const double r = rsqrt(sum * p.inv_hidden + p.eps);
+  const float rf = (float)r;
+  // a thread reads what it has written itself
+  auto normed = [&](int c, float (&n)[8]) {
     const int m = p.hidden - c;
+    float s[8];
     if constexpr (RES) {
       const Cols8<S> a = load_cols(static_cast<const S*>(total) + c, m);
 #pragma unroll
@@ -152,148 +356,95 @@ __global__ __launch_bounds__(kWave*(W < 4 ? 4 : W)) void rmsnorm_kernel(NormPara
 #pragma unroll
       for (int i = 0; i < 8; ++i) s[i] = static_cast<float>(a.v[i]);
     }
-  };
-
-  const int c0 = 8 * t;
-  double sum = 0;
-  float s[8] = {};
-  Weight8 w{};
-  if (c0 < p.hidden) {
-    w = load_weight(p, c0, p.hidden - c0);
-    open(c0, s);
-  }
-  if (LONG)
-    for (int c = c0 + kSpan; c < p.hidden; c += kSpan) {
-      float v[8];
-      open(c, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) sum = fma((double)v[i], (double)v[i], sum);
-    }
-#pragma unroll
-  for (int i = 0; i < 8; ++i) sum = fma((double)s[i], (double)s[i], sum);
-  sum = wave_sum(sum);
-  if (W > 1) {
-    if (t % kWave == 0) part[wave] = sum;
-    __syncthreads();
-    sum = 0;
-#pragma unroll
-    for (int i = 0; i < W; ++i) sum += part[i];
-  }
-  const double r = rsqrt(sum * p.inv_hidden + p.eps);
-  const float rf = (float)r;
-  auto normed = [&](const float (&v)[8], const Weight8& wv, float (&n)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float wi = wv.at(i, p.w_bf16);
-      n[i] = kBf16 ? v[i] * rf * wi : (float)((double)v[i] * r * (double)wi);
+      const float w = i < m ? weight_at(p.weight, p.w_bf16, c + i) : 0.0f;
+      n[i] = kBf16 ? s[i] * rf * w : (float)((double)s[i] * r * (double)w);
     }
   };
-
-  // a row's own scale
   uint32_t top = 0;
-  float n[8];
-  normed(s, w, n);
   if (kInt8) {
+    for (int c = 8 * threadIdx.x; c < p.hidden; c += kSpan) {
+      float n[8];
+      normed(c, n);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) top = max(top, magnitude(n[i]));
-    if (LONG)
-      for (int c = c0 + kSpan; c < p.hidden; c += kSpan) {
-        float v[8], nv[8];
-        again(c, v);
-        normed(v, load_weight(p, c, p.hidden - c), nv);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, magnitude(nv[i]));
-      }
-    top = wave_max(top);
-    if (W > 1) {
-      if (t % kWave == 0) part_top[wave] = top;
-      __syncthreads();
-#pragma unroll
-      for (int i = 0; i < W; ++i) top = max(top, part_top[i]);
+      for (int i = 0; i < 8; ++i) top = max(top, magnitude(n[i]));
     }
+    top = wave_max(top);
+    if (threadIdx.x % kWave == 0) part_top[threadIdx.x / kWave] = top;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < W; ++i) top = max(top, part_top[i]);
+    if (threadIdx.x == 0) static_cast<float*>(p.scale)[row] = int8_scale(top);
   }
-  const float a = __uint_as_float(top);
-  const bool finite = top < 0x7F800000u;
-  const float inv = 127.0f / a;
-  if (kInt8 && t == 0)
-    static_cast<float*>(p.scale)[row] = finite ? a / 127.0f : __uint_as_float(0x7FC00000u);
-
-  auto close = [&](int c, const float (&nv)[8]) {
-    if constexpr (kInt8) {
-      if (c >= p.hidden) return;
-      uint32_t o[2] = {0, 0};
-      if (finite && top != 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-          o[i / 4] |= (uint32_t)(quantized(nv[i], a, inv) & 0xFF) << (8 * (i % 4));
-      }
-      __builtin_memcpy(static_cast<int8_t*>(p.y) + row * p.hidden + c, o, 8);
-    } else if constexpr (kMx) {
-      // a wavefront's columns are one word of scales, its padding included
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m = max(m, magnitude(nv[i]));
-      const uint32_t byte = mxfp4_byte(block_max(m));
-      if (c / 512 * 512 < p.hidden && threadIdx.x % 4 == 0)
-        static_cast<uint8_t*>(p.scale)[((c / 512) * p.n_rows + row) * 16 + c / 32 % 16] =
-            c < p.hidden ? byte : 0;
-      if (c < p.hidden) {
-        const uint32_t codes = mxfp4_codes(nv, byte);
-        *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * (p.hidden / 2) + c / 2) =
-            codes;
-      }
-    } else {
-      if (c >= p.hidden) return;
+  for (int c = 8 * threadIdx.x; c < (p.hidden + 511) / 512 * 512; c += kSpan) {
+    float n[8] = {};
+    if (c < p.hidden) normed(c, n);
+    if constexpr (kMx) {
+      store_mxfp4<false>(p, row, c, n);
+    } else if constexpr (kInt8) {
+      if (c < p.hidden) store_int8<false>(p, row, c, n, top);
+    } else if (c < p.hidden) {
       Cols8<O> o;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o.v[i] = static_cast<O>(nv[i]);
+      for (int i = 0; i < 8; ++i) o.v[i] = static_cast<O>(n[i]);
       store_cols(static_cast<O*>(p.y) + row * p.y_stride + c, o, p.hidden - c);
     }
-  };
-  close(c0, n);
-  if (LONG)
-    for (int c = c0 + kSpan; c < (p.hidden + 511) / 512 * 512; c += kSpan) {
-      float v[8] = {}, nv[8];
-      Weight8 wv{};
-      if (c < p.hidden) {
-        again(c, v);
-        wv = load_weight(p, c, p.hidden - c);
-      }
-      normed(v, wv, nv);
-      close(c, nv);
-    }
+  }
 }
 
 // A launch takes fewer than 2^32 threads.
 constexpr int64_t kRowsPerLaunch = 1 << 21;
 
+// With few rows eight columns a lane, so that a row's pass is short; with many
+// 64 bytes a lane, so that a CU has enough of them in flight.  Rows are many
+// from these bytes of x on (us, few / many, the residual added: bf16 512 x 4096
+// 6.2 / 6.8, 1024 x 4096 9.5 / 8.0, 256 x 7168 6.0 / 6.4, 512 x 7168 9.4 / 8.0;
+// fp32 128 x 4096 4.6 / 4.3, 256 x 4096 7.0 / 5.6, 1024 x 4096 21.4 / 13.1).
+template <typename X, typename S>
+bool many_rows(int64_t n_rows, int hidden) {
+  constexpr bool kBf16 = sizeof(X) == 2 && sizeof(S) == 2;
+  return n_rows * hidden * (int64_t)sizeof(X) >= (kBf16 ? 5 << 20 : 3 << 20);
+}
+// Workgroups that share many rows: four a CU (4096 x 4096 to int8 23.0 us, three
+// a CU 24.4, two 31.9).
+constexpr int kGroups = 256 * 4;
+
 template <typename X, typename S, bool RES, typename O>
 hipError_t launch_norm(NormParams p, hipStream_t stream) {
-  const int vectors = (p.hidden + 7) / 8;
-  for (; p.row0 < p.n_rows; p.row0 += kRowsPerLaunch) {
-    const int64_t left = p.n_rows - p.row0;
-    const unsigned rows = (unsigned)(left < kRowsPerLaunch ? left : kRowsPerLaunch);
-    NormParams q = p;
-    q.n_rows = p.n_rows;
-    if (vectors <= kWave)
-      hipLaunchKernelGGL((rmsnorm_kernel<X, S, RES, O, 1, false>), dim3((rows + 3) / 4),
-                         dim3(4 * kWave), 0, stream, q);
-    else if (vectors <= 4 * kWave)
-      hipLaunchKernelGGL((rmsnorm_kernel<X, S, RES, O, 4, false>), dim3(rows), dim3(4 * kWave), 0,
-                         stream, q);
-    else if (vectors <= 8 * kWave)
-      hipLaunchKernelGGL((rmsnorm_kernel<X, S, RES, O, 8, false>), dim3(rows), dim3(8 * kWave), 0,
-                         stream, q);
-    else if (vectors <= 16 * kWave)
-      hipLaunchKernelGGL((rmsnorm_kernel<X, S, RES, O, 16, false>), dim3(rows), dim3(16 * kWave),
-                         0, stream, q);
-    else
-      hipLaunchKernelGGL((rmsnorm_kernel<X, S, RES, O, 16, true>), dim3(rows), dim3(16 * kWave),
-                         0, stream, q);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
+  const int64_t n = p.n_rows;
+  if (p.hidden > 8192 || p.hidden < 8) {
+    for (; p.row0 < n; p.row0 += kRowsPerLaunch) {
+      const unsigned rows = (unsigned)(n - p.row0 < kRowsPerLaunch ? n - p.row0 : kRowsPerLaunch);
+      hipLaunchKernelGGL((rmsnorm_long_kernel<X, S, RES, O>), dim3(rows), dim3(16 * kWave), 0,
+                         stream, p);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
   }
-  return hipSuccess;
+  const int vectors = (p.hidden + 7) / 8;
+  constexpr int V = sizeof(X) == 4 || sizeof(S) == 4 ? 2 : 4;
+  const bool many = many_rows<X, S>(n, p.hidden);
+  auto launch = [&](auto kernel, int64_t groups, int waves) {
+    hipLaunchKernelGGL(kernel, dim3((unsigned)(groups < kGroups ? groups : kGroups)),
+                       dim3(waves * kWave), 0, stream, p);
+  };
+  if (vectors <= kWave)
+    launch(rmsnorm_kernel<X, S, RES, O, 1, 1>, (n + 3) / 4, 4);
+  else if (many && vectors <= kWave * V)
+    launch(rmsnorm_kernel<X, S, RES, O, 1, V>, (n + 3) / 4, 4);
+  else if (many && vectors <= 2 * kWave * V)
+    launch(rmsnorm_kernel<X, S, RES, O, 2, V>, n, 2);
+  else if (many && vectors <= 4 * kWave * V)
+    launch(rmsnorm_kernel<X, S, RES, O, 4, V>, n, 4);
+  else if (vectors <= 4 * kWave)
+    launch(rmsnorm_kernel<X, S, RES, O, 4, 1>, n, 4);
+  else if (vectors <= 8 * kWave)
+    launch(rmsnorm_kernel<X, S, RES, O, 8, 1>, n, 8);
+  else
+    launch(rmsnorm_kernel<X, S, RES, O, 16, 1>, n, 16);
+  return hipGetLastError();
 }
 
 template <typename O>
@@ -350,61 +501,83 @@ struct BackParams {
   int groups;
 };
 
-__device__ __forceinline__ Weight8 load_weight(const BackParams& p, int c, int m) {
-  NormParams q{};
-  q.weight = p.weight;
-  q.w_bf16 = p.w_bf16;
-  return load_weight(q, c, m);
+// The bytes of eight columns as they are, to be converted again where they are
+// used again: sixteen floats more a lane do not fit.
+template <typename T>
+__device__ __forceinline__ void keep_stored(Cols8<T>& r) {
+  uint32_t b[sizeof(r) / 4];
+  __builtin_memcpy(b, &r, sizeof(r));
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r) / 4; ++i) asm volatile("" : "+v"(b[i]));
+  __builtin_memcpy(&r, b, sizeof(r));
 }
 
-// W wavefronts a row, eight columns a lane, a workgroup takes every
-// gridDim.x-th row (by fours where a row is one wavefront) and keeps its
-// columns' part of dweight in registers.  The next row is loaded while the
-// sums of this one go through the workgroup.
-template <typename D, typename S, bool TOT, int W>
-__global__ __launch_bounds__(kWave*(W < 4 ? 4 : W)) void rmsnorm_back_kernel(BackParams p) {
-  constexpr int kRows = W < 4 ? 4 / W : 1;
-  __shared__ double part[2][W][2];
-  __shared__ float wide[W == 1 ? 4 * kWave * 8 : 1];
-  const int t = threadIdx.x % (W * kWave), wave = t / kWave;
+// NW wavefronts a workgroup, W of them a row, V times eight columns a lane: NW
+// / W rows at a time, of every NW gridDim.x / W, and the columns' part of
+// dweight stays in registers, so that a workgroup writes one part.  The next
+// rows are loaded while the sums of these go through the workgroup.
+constexpr int kBackWaves = 16;  // of a workgroup that takes many rows
+template <typename D, typename S, bool TOT, int W, int V, int NW>
+__global__ __launch_bounds__(kWave* NW) void rmsnorm_back_kernel(BackParams p) {
+  constexpr int kRows = NW / W;
+  constexpr int kSpan = W * kWave * 8;
+  __shared__ double part[2][NW][2];
+  __shared__ float wide[kRows > 1 ? NW * kWave * 8 : 1];
+  const int t = threadIdx.x % (W * kWave), wave = threadIdx.x / kWave;
   const int sub = threadIdx.x / (W * kWave);
-  const int c = 8 * t, m = p.hidden - c;
-  float w[8] = {}, acc[8] = {};
-  if (m > 0) {
-    const Weight8 wv = load_weight(p, c, m);
+  const int c0 = 8 * t;
+  float w[V][8] = {}, acc[V][8] = {};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = wv.at(i, p.w_bf16);
+  for (int v = 0; v < V; ++v) {
+    const Weight8 wv = load_weight(p.weight, p.w_bf16, Columns(c0 + v * kSpan, p.hidden).c);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[v][i] = wv.at(i, p.w_bf16);
   }
-  Cols8<D> dy{};
-  Cols8<S> sv{}, tv{};
-  auto load = [&](int64_t row) {
-    if (m <= 0 || row >= p.n_rows) return;
-    dy = load_cols(static_cast<const D*>(p.dy) + row * p.dy_stride + c, m);
-    sv = load_cols(static_cast<const S*>(p.s) + row * p.s_stride + c, m);
-    if (TOT) tv = load_cols(static_cast<const S*>(p.dtotal) + row * p.dtotal_stride + c, m);
+  Cols8<D> dy[V];
+  Cols8<S> sv[V];
+  auto load = [&](int64_t row) {  // the last row again behind the last
+    row = row < p.n_rows ? row : p.n_rows - 1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int c = Columns(c0 + v * kSpan, p.hidden).c;
+      dy[v] = load_cols(static_cast<const D*>(p.dy) + row * p.dy_stride + c);
+      sv[v] = load_cols(static_cast<const S*>(p.s) + row * p.s_stride + c);
+    }
   };
+  const int64_t step = (int64_t)gridDim.x * kRows;
   int64_t row = (int64_t)blockIdx.x * kRows + sub;
   load(row);
   int turn = 0;
-  for (; row < p.n_rows; row += (int64_t)gridDim.x * kRows) {
-    float d[8], s[8], tot[8];
+  // every wavefront takes as many turns as the workgroup's first row
+  for (int64_t first = (int64_t)blockIdx.x * kRows; first < p.n_rows; first += step, row += step) {
+    Cols8<D> d[V];
+    Cols8<S> s[V], tot[V];
     double ss = 0, sg = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      d[i] = static_cast<float>(dy.v[i]);
-      s[i] = static_cast<float>(sv.v[i]);
-      tot[i] = TOT ? static_cast<float>(tv.v[i]) : 0.0f;
+    for (int v = 0; v < V; ++v) {
+      d[v] = dy[v];
+      s[v] = sv[v];
+      if (TOT)
+        tot[v] = load_cols(static_cast<const S*>(p.dtotal) +
+                           (row < p.n_rows ? row : p.n_rows - 1) * p.dtotal_stride +
+                           Columns(c0 + v * kSpan, p.hidden).c);
     }
-    load(row + (int64_t)gridDim.x * kRows);
+    load(row + step);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      ss = fma((double)s[i], (double)s[i], ss);
-      sg = fma((double)s[i], (double)(w[i] * d[i]), sg);
+    for (int v = 0; v < V; ++v) {
+      const Columns at(c0 + v * kSpan, p.hidden);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float si = i < at.skip ? 0.0f : static_cast<float>(s[v].v[i]);
+        const float gi = i < at.skip ? 0.0f : w[v][i] * static_cast<float>(d[v].v[i]);
+        ss = fma((double)si, (double)si, ss);
+        sg = fma((double)si, (double)gi, sg);
+      }
     }
     ss = wave_sum(ss);
     sg = wave_sum(sg);
     if (W > 1) {
-      if (t % kWave == 0) {
+      if (threadIdx.x % kWave == 0) {
         part[turn][wave][0] = ss;
         part[turn][wave][1] = sg;
       }
@@ -412,44 +585,62 @@ __global__ __launch_bounds__(kWave*(W < 4 ? 4 : W)) void rmsnorm_back_kernel(Bac
       ss = sg = 0;
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        ss += part[turn][i][0];
-        sg += part[turn][i][1];
+        ss += part[turn][sub * W + i][0];
+        sg += part[turn][sub * W + i][1];
       }
       turn ^= 1;
     }
+    if (row >= p.n_rows) continue;
+    if (V > 1)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        keep_stored(d[v]);
+        keep_stored(s[v]);
+      }
     const double r = rsqrt(ss * p.inv_hidden + p.eps);
     const float rf = (float)r, k = (float)(r * r * r * sg * p.inv_hidden);
-    if (m > 0) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
       Cols8<S> o;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        float v = rf * (w[i] * d[i]) - k * s[i];
-        if (TOT) v += tot[i];
-        o.v[i] = static_cast<S>(v);
-        acc[i] += d[i] * s[i] * rf;
+        const float di = static_cast<float>(d[v].v[i]), si = static_cast<float>(s[v].v[i]);
+        float g = rf * (w[v][i] * di) - k * si;
+        if (TOT) g += static_cast<float>(tot[v].v[i]);
+        o.v[i] = static_cast<S>(g);
+        acc[v][i] += di * si * rf;
       }
-      store_cols(static_cast<S*>(p.dx) + row * p.dx_stride + c, o, m);
+      store_own<(kRows > 1)>(static_cast<S*>(p.dx) + row * p.dx_stride,
+                             Columns(c0 + v * kSpan, p.hidden), o);
     }
   }
   if (p.dw == nullptr) return;
-  if (W == 1) {
+  float* const dw = p.dw + (int64_t)blockIdx.x * p.hidden;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) wide[sub * 512 + 8 * t + i] = acc[i];
-    __syncthreads();
-    for (int j = threadIdx.x; j < p.hidden; j += 4 * kWave)
-      p.dw[(int64_t)blockIdx.x * p.hidden + j] =
-          (wide[j] + wide[512 + j]) + (wide[1024 + j] + wide[1536 + j]);
-    return;
-  }
-  if (m > 0) {
-    Cols8<float> o;
+  for (int v = 0; v < V; ++v) {
+    const Columns at(c0 + v * kSpan, p.hidden);
+    if (kRows > 1) {
+      __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o.v[i] = acc[i];
-    store_cols(p.dw + (int64_t)blockIdx.x * p.hidden + c, o, m);
+      for (int i = 0; i < 8; ++i)
+        if (i >= at.skip) wide[sub * kSpan + at.c - v * kSpan + i] = acc[v][i];
+      __syncthreads();
+      for (int j = threadIdx.x; j < kSpan && v * kSpan + j < p.hidden; j += kWave * NW) {
+        double sum = 0;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) sum += (double)wide[i * kSpan + j];
+        dw[v * kSpan + j] = (float)sum;
+      }
+    } else {
+      Cols8<float> o;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o.v[i] = acc[v][i];
+      store_own<false>(dw, at, o);
+    }
   }
 }
 
-// Rows longer than the registers hold: the sums in one pass, dx in a second;
+// Rows longer than the registers hold, or shorter than eight columns: the sums in one pass, dx in a second;
 // r goes to memory for dweight, which another kernel takes by columns.
 template <typename D, typename S, bool TOT>
 __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParams p) {
@@ -465,12 +656,14 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParam
     const int m = p.hidden - c;
     const Cols8<D> d = load_cols(dy + c, m);
     const Cols8<S> v = load_cols(s + c, m);
-    const Weight8 w = load_weight(p, c, m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float si = static_cast<float>(v.v[i]);
       ss = fma((double)si, (double)si, ss);
-      sg = fma((double)si, (double)(w.at(i, p.w_bf16) * static_cast<float>(d.v[i])), sg);
+      sg = fma((double)si,
+               (double)((i < m ? weight_at(p.weight, p.w_bf16, c + i) : 0.0f) *
+                        static_cast<float>(d.v[i])),
+               sg);
     }
   }
   ss = wave_sum(ss);
@@ -493,12 +686,12 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParam
     const int m = p.hidden - c;
     const Cols8<D> d = load_cols(dy + c, m);
     const Cols8<S> v = load_cols(s + c, m);
-    const Weight8 w = load_weight(p, c, m);
     Cols8<S> tv{}, o;
     if (TOT) tv = load_cols(tot + c, m);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      float g = rf * (w.at(i, p.w_bf16) * static_cast<float>(d.v[i])) - k * static_cast<float>(v.v[i]);
+      const float w = i < m ? weight_at(p.weight, p.w_bf16, c + i) : 0.0f;
+      float g = rf * (w * static_cast<float>(d.v[i])) - k * static_cast<float>(v.v[i]);
       if (TOT) g += static_cast<float>(tv.v[i]);
       o.v[i] = static_cast<S>(g);
     }
@@ -518,13 +711,13 @@ __global__ __launch_bounds__(256) void rmsnorm_back_columns_kernel(BackParams p)
   p.dw[(int64_t)blockIdx.y * p.hidden + c] = acc;
 }
 
-// dweight from the workgroups' parts: 16 columns a workgroup, every 16th part
-// a thread.
-__global__ __launch_bounds__(256) void rmsnorm_back_join_kernel(const float* parts, int groups,
+// dweight from the workgroups' parts: 32 columns a workgroup, whole lines of
+// each part, every 16th part a thread.
+__global__ __launch_bounds__(512) void rmsnorm_back_join_kernel(const float* parts, int groups,
                                                                 int hidden, float* dweight) {
-  __shared__ double sums[16][17];
-  const int col = threadIdx.x % 16, g = threadIdx.x / 16;
-  const int c = blockIdx.x * 16 + col;
+  __shared__ double sums[16][33];
+  const int col = threadIdx.x % 32, g = threadIdx.x / 32;
+  const int c = blockIdx.x * 32 + col;
   double acc = 0;
   if (c < hidden) {
 #pragma unroll 8
@@ -538,10 +731,26 @@ __global__ __launch_bounds__(256) void rmsnorm_back_join_kernel(const float* par
   }
 }
 
+// Columns a lane by eights where a workgroup takes several rows: 32 bytes.
+constexpr int back_vectors(bool bf16) { return bf16 ? 2 : 1; }
+
+// Rows of which a workgroup takes one at a time (us, one / several, dtotal
+// added: bf16 512 x 4096 11.4 / 12.7, 1536 x 4096 18.0 / 18.5, 2048 x 4096 21.7
+// / 21.2, 1536 x 1024 11.4 / 12.9, 2048 x 1024 13.0 / 11.6; fp32 512 x 1024 8.1
+// / 9.0, 1024 x 1024 10.6 / 9.1, 512 x 4096 13.7 / 12.7, 1024 x 4096 20.7 /
+// 18.5).
+bool back_few(bool bf16, int64_t n_rows) { return n_rows <= (bf16 ? 1536 : 512); }
+
+// Wavefronts a row, V times eight columns a lane.
+int back_waves(int v, int hidden) {
+  int w = 1;
+  while (w * kWave * 8 * v < hidden) w *= 2;
+  return w;
+}
+
 template <typename D, typename S, bool TOT>
 hipError_t launch_back(BackParams p, hipStream_t stream) {
-  const int vectors = (p.hidden + 7) / 8;
-  if (p.hidden > kNormBackCols) {
+  if (norm_back_long(p.hidden)) {
     const int64_t n = p.n_rows;
     for (int64_t r = 0; r < n; r += kRowsPerLaunch) {
       BackParams q = p;
@@ -559,18 +768,31 @@ hipError_t launch_back(BackParams p, hipStream_t stream) {
     if (p.dw != nullptr)
       hipLaunchKernelGGL((rmsnorm_back_columns_kernel<D, S>),
                          dim3((p.hidden + 255) / 256, p.groups), dim3(256), 0, stream, p);
-  } else if (vectors <= kWave) {
-    hipLaunchKernelGGL((rmsnorm_back_kernel<D, S, TOT, 1>), dim3(p.groups), dim3(4 * kWave), 0,
-                       stream, p);
-  } else if (vectors <= 4 * kWave) {
-    hipLaunchKernelGGL((rmsnorm_back_kernel<D, S, TOT, 4>), dim3(p.groups), dim3(4 * kWave), 0,
-                       stream, p);
-  } else if (vectors <= 8 * kWave) {
-    hipLaunchKernelGGL((rmsnorm_back_kernel<D, S, TOT, 8>), dim3(p.groups), dim3(8 * kWave), 0,
-                       stream, p);
   } else {
-    hipLaunchKernelGGL((rmsnorm_back_kernel<D, S, TOT, 16>), dim3(p.groups), dim3(16 * kWave), 0,
-                       stream, p);
+    constexpr bool kBf16 = sizeof(D) == 2 && sizeof(S) == 2;
+    constexpr int V = back_vectors(kBf16);
+    auto launch = [&](auto kernel, int waves) {
+      hipLaunchKernelGGL(kernel, dim3(p.groups), dim3(waves * kWave), 0, stream, p);
+    };
+    if (back_few(kBf16, p.n_rows)) {  // a row as wide as it can be
+      const int w = back_waves(1, p.hidden);
+      if (w <= 4)
+        launch(rmsnorm_back_kernel<D, S, TOT, 4, 1, 4>, 4);
+      else if (w == 8)
+        launch(rmsnorm_back_kernel<D, S, TOT, 8, 1, 8>, 8);
+      else
+        launch(rmsnorm_back_kernel<D, S, TOT, 16, 1, 16>, 16);
+      return hipGetLastError();
+    }
+    switch (back_waves(V, p.hidden)) {
+      case 1: launch(rmsnorm_back_kernel<D, S, TOT, 1, V, kBackWaves>, kBackWaves); break;
+      case 2: launch(rmsnorm_back_kernel<D, S, TOT, 2, V, kBackWaves>, kBackWaves); break;
+      case 4: launch(rmsnorm_back_kernel<D, S, TOT, 4, V, kBackWaves>, kBackWaves); break;
+      case 8: launch(rmsnorm_back_kernel<D, S, TOT, 8, V, kBackWaves>, kBackWaves); break;
+      default:
+        if constexpr (V == 1)
+          launch(rmsnorm_back_kernel<D, S, TOT, 16, V, kBackWaves>, kBackWaves);
+    }
   }
   return hipGetLastError();
 }
@@ -627,13 +849,20 @@ moe_status moe_rmsnorm_backward(const void* dy, int dy_type, int64_t dy_stride, 
   p.dx = dx;
   p.dx_stride = dx_stride;
   p.groups = moe::norm_back_groups(n_rows, hidden);
+  const bool bf16 = dy_type == MOE_ACT_BF16 && s_type == MOE_ACT_BF16;
+  if (!moe::norm_back_long(hidden) && !moe::back_few(bf16, n_rows)) {
+    // fewer where a workgroup takes several rows at once
+    const int rows = moe::kBackWaves / moe::back_waves(moe::back_vectors(bf16), hidden);
+    const int all = (n_rows + rows - 1) / rows;
+    if (all < p.groups) p.groups = all;
+  }
   float* const parts = dweight == nullptr ? nullptr
                                           : reinterpret_cast<float*>(
                                                 static_cast<char*>(workspace) +
                                                 moe::norm_inv_bytes(n_rows, hidden));
   // a single group's part is dweight
   p.dw = p.groups == 1 && dweight != nullptr ? dweight : parts;
-  if (dweight != nullptr && hidden > moe::kNormBackCols) p.inv = static_cast<float*>(workspace);
+  if (dweight != nullptr && moe::norm_back_long(hidden)) p.inv = static_cast<float*>(workspace);
   hipError_t e = hipSuccess;
   if (n_rows > 0) {
     const bool db = dy_type == MOE_ACT_BF16, sb = s_type == MOE_ACT_BF16, t = dtotal != nullptr;
@@ -651,7 +880,7 @@ moe_status moe_rmsnorm_backward(const void* dy, int dy_type, int64_t dy_stride, 
             : moe::launch_back<float, float, false>(p, stream);
   }
   if (e == hipSuccess && dweight != nullptr && p.groups != 1) {
-    hipLaunchKernelGGL(moe::rmsnorm_back_join_kernel, dim3((hidden + 15) / 16), dim3(256), 0,
+    hipLaunchKernelGGL(moe::rmsnorm_back_join_kernel, dim3((hidden + 31) / 32), dim3(512), 0,
                        stream, parts, p.groups, hidden, dweight);
     e = hipGetLastError();
   }

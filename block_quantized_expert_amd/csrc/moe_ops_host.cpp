@@ -215,16 +215,12 @@ moe_status check_rmsnorm_mxfp4(const moe_norm_rows* rows, const uint8_t* codes,
 }
 
 int norm_back_groups(int64_t n_rows, int hidden) {
-  if (n_rows == 0) return 0;
-  if (hidden > kNormBackCols) return (int)(n_rows < 64 ? n_rows : 64);
-  const int64_t rows = hidden <= 512 ? 4 : 1;  // that a workgroup has at a time
-  const int64_t most = hidden <= 4096 ? 512 : 256;
-  const int64_t all = (n_rows + rows - 1) / rows;
-  return (int)(all < most ? all : most);
+  const int64_t most = norm_back_long(hidden) ? 64 : 256;
+  return (int)(n_rows < most ? n_rows : most);
 }
 
 size_t norm_inv_bytes(int64_t n_rows, int hidden) {
-  return hidden > kNormBackCols ? (size_t)(n_rows + 1) / 2 * 8 : 0;
+  return norm_back_long(hidden) ? (size_t)(n_rows + 1) / 2 * 8 : 0;
 }
 
 moe_status check_rmsnorm_backward(const void* dy, int dy_type, int64_t dy_stride, const void* s,

@@ -45,10 +45,11 @@ moe_status check_rmsnorm_backward(const void* dy, int dy_type, int64_t dy_stride
                                   int hidden, float eps, const void* dx, int64_t dx_stride,
                                   const float* dweight, const void* workspace,
                                   size_t workspace_bytes);
-// The norm's gradients: columns of a row that stays in registers, workgroups
-// that share the rows (each with a part of dweight), bytes of the longer rows'
-// r in front of those parts.
+// The norm's gradients: rows that do not stay in registers, the most
+// workgroups that share the rows (each with a part of dweight), bytes of those
+// rows' r in front of the parts.
 constexpr int kNormBackCols = 8192;
+constexpr bool norm_back_long(int hidden) { return hidden > kNormBackCols || hidden < 8; }
 int norm_back_groups(int64_t n_rows, int hidden);
 size_t norm_inv_bytes(int64_t n_rows, int hidden);
 // Rounding and its inverse alike.
