@@ -30,14 +30,14 @@ struct CastParams {
   int lanes;  // of a row in a wavefront: 64, or as many as a short row needs (a power of two)
 };
 
-// The row, word and first of eight columns of this lane; a wavefront takes
-// one word of a row, or all of several short rows.
+// The row, word and first of eight columns of this lane in the launch's
+// `unit`: one word of a row, or all of several short rows.
 struct Place {
   int64_t row;
   int word, c, lane;  // lane: within the row
+  bool in;            // the columns are the row's
 };
-__device__ __forceinline__ Place cast_place(const CastParams& p) {
-  const uint32_t unit = blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+__device__ __forceinline__ Place cast_place(const CastParams& p, uint32_t unit) {
   const int lane = threadIdx.x % kWave;
   const uint32_t group = unit / p.words;
   Place at;
@@ -45,46 +45,61 @@ __device__ __forceinline__ Place cast_place(const CastParams& p) {
   at.lane = lane & (p.lanes - 1);
   at.row = p.row0 + (int64_t)group * (kWave / p.lanes) + lane / p.lanes;
   at.c = at.word * 512 + 8 * at.lane;
+  at.in = at.row < p.n_rows && at.c < p.cols;
   return at;
 }
-
-template <typename T>
-__global__ __launch_bounds__(kThreads) void quantize_kernel(CastParams p) {
-  const Place at = cast_place(p);
-  const bool in = at.row < p.n_rows && at.c < p.cols;
-  float v[8] = {};
-  if (in) {
-    const Cols8<T> r = load_cols(static_cast<const T*>(p.x) + at.row * p.x_stride + at.c);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = static_cast<float>(r.v[i]);
-  }
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, magnitude(v[i]));
-  const uint32_t byte = mxfp4_byte(block_max(top));
-  if (in) {
-    const uint32_t codes = mxfp4_codes(v, byte);
-    *reinterpret_cast<uint32_t*>(p.codes + at.row * (p.cols / 2) + at.c / 2) = codes;
-  }
-  // lane i < 4 of a row stores bytes 4i .. 4i + 3 of the row's word, which its
-  // lanes 16i, 16i + 4, ... hold; past the row's end they are 0
-  uint32_t word = 0;
-  const int first = threadIdx.x % kWave - at.lane;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int from = 16 * at.lane + 4 * b;
-    const uint32_t got = __shfl((int)(in ? byte : 0u), (first + from) % kWave);
-    word |= (from < p.lanes ? got : 0u) << (8 * b);
-  }
-  if (at.lane < 4 && at.row < p.n_rows)
-    *reinterpret_cast<uint32_t*>(p.scales + (at.word * p.n_rows + at.row) * 16 + 4 * at.lane) =
-        word;
+__device__ __forceinline__ uint32_t cast_unit(int units) {
+  return (blockIdx.x * kWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave)) * units;
 }
 
-template <typename T>
+template <typename T, int U>
+__global__ __launch_bounds__(kThreads) void quantize_kernel(CastParams p) {
+  Place at[U];
+  Cols8<T> r[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {  // without a branch, so that all are under way at once
+    at[u] = cast_place(p, cast_unit(U) + u);
+    r[u] = load_cols(static_cast<const T*>(p.x) +
+                     (at[u].in ? at[u].row * p.x_stride + at[u].c : 0));
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    float v[8];
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = static_cast<float>(r[u].v[i]);
+      top = max(top, magnitude(v[i]));
+    }
+    const uint32_t byte = mxfp4_byte(block_max(top));
+    const uint32_t codes = mxfp4_codes(v, byte);
+    auto* const to = reinterpret_cast<uint32_t*>(p.codes + at[u].row * (p.cols / 2) + at[u].c / 2);
+    if (at[u].in) {
+      if (U > 1)
+        __builtin_nontemporal_store(codes, to);
+      else
+        *to = codes;
+    }
+    // lane i < 4 of a row stores bytes 4i .. 4i + 3 of the row's word, which its
+    // lanes 16i, 16i + 4, ... hold; past the row's end they are 0
+    uint32_t word = 0;
+    const int first = threadIdx.x % kWave - at[u].lane;
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+      const int from = 16 * at[u].lane + 4 * b;
+      const uint32_t got = __shfl((int)(at[u].in ? byte : 0u), (first + from) % kWave);
+      word |= (from < p.lanes ? got : 0u) << (8 * b);
+    }
+    if (at[u].lane < 4 && at[u].row < p.n_rows)
+      *reinterpret_cast<uint32_t*>(p.scales + (at[u].word * p.n_rows + at[u].row) * 16 +
+                                   4 * at[u].lane) = word;
+  }
+}
+
+template <typename T, bool PAST>
 __global__ __launch_bounds__(kThreads) void dequantize_kernel(CastParams p) {
-  const Place at = cast_place(p);
-  if (at.row >= p.n_rows || at.c >= p.cols) return;
+  const Place at = cast_place(p, cast_unit(1));
+  if (!at.in) return;
   const uint32_t w =
       *reinterpret_cast<const uint32_t*>(p.codes + at.row * (p.cols / 2) + at.c / 2);
   const uint32_t byte = p.scales[(at.word * p.n_rows + at.row) * 16 + at.lane / 4];
@@ -95,11 +110,27 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(CastParams p) {
     const float f = byte == 255 ? __uint_as_float(0x7FC00000u) : static_cast<float>(v[i]);
     o.v[i] = static_cast<T>(f);
   }
-  store_cols(static_cast<T*>(p.x) + at.row * p.x_stride + at.c, o, 8);
+  T* const to = static_cast<T*>(p.x) + at.row * p.x_stride + at.c;
+  if (PAST)
+    store_past(to, o);
+  else
+    __builtin_memcpy(to, &o, sizeof(o));
 }
 
-template <typename F>
-moe_status cast(CastParams p, F launch) {
+// Large casts of bf16 rows (us, 4096 and 8192 rows of 4096): to MXFP4 a
+// wavefront takes four words, their loads at once and the codes past the caches
+// (10.5 -> 9.5, 20.4 -> 17.4; 2048 rows 6.7 -> 6.3, 1024 rows 4.5 -> 4.7); back,
+// the rows go past the caches (9.6 -> 8.3, 19.9 -> 14.2; 2048 rows 6.5 -> 5.4).
+// fp32 rows gain nothing (4096 rows to MXFP4 15.6 and 15.0) or lose: a lane's 32
+// bytes are two stores, and half lines past the caches take 23 us, not 19.
+constexpr int kCastUnits = 4;
+bool large_cast(const CastParams& p, int type) {
+  return type == MOE_ACT_BF16 && p.n_rows * p.cols >= 1 << 23;
+}
+
+// `units`: a wavefront's.
+template <typename K>
+moe_status cast(K kernel, CastParams p, int units, hipStream_t stream) {
   p.words = MOE_MXFP4_WORDS(p.cols);
   p.lanes = 4;
   while (p.lanes < kWave && 8 * p.lanes < p.cols) p.lanes *= 2;
@@ -108,8 +139,9 @@ moe_status cast(CastParams p, F launch) {
   const int64_t most = (int64_t{1} << 25) / p.words * per;
   for (p.row0 = 0; p.row0 < p.n_rows; p.row0 += most) {
     const int64_t rows = p.n_rows - p.row0 < most ? p.n_rows - p.row0 : most;
-    const int64_t units = (rows + per - 1) / per * p.words;
-    launch(p, dim3((unsigned)((units + kWaves - 1) / kWaves)));
+    const int64_t all = (rows + per - 1) / per * p.words, each = kWaves * units;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((all + each - 1) / each)), dim3(kThreads), 0, stream,
+                       p);
     if (hipGetLastError() != hipSuccess) return MOE_ERR_DEVICE;
   }
   return MOE_OK;
@@ -839,12 +871,10 @@ moe_status moe_quantize_mxfp4(const void* x, int x_type, int64_t x_stride, int n
   const moe_status s = moe::check_mxfp4_rows(x, x_type, x_stride, n_rows, cols, codes, scales);
   if (s != MOE_OK || n_rows == 0) return s;
   moe::CastParams p{const_cast<void*>(x), x_stride, codes, scales, n_rows, 0, cols, 0, 0};
-  return moe::cast(p, [&](const moe::CastParams& q, dim3 grid) {
-    if (x_type == MOE_ACT_BF16)
-      hipLaunchKernelGGL((moe::quantize_kernel<__bf16>), grid, dim3(moe::kThreads), 0, stream, q);
-    else
-      hipLaunchKernelGGL((moe::quantize_kernel<float>), grid, dim3(moe::kThreads), 0, stream, q);
-  });
+  if (moe::large_cast(p, x_type))
+    return moe::cast(moe::quantize_kernel<__bf16, moe::kCastUnits>, p, moe::kCastUnits, stream);
+  return x_type == MOE_ACT_BF16 ? moe::cast(moe::quantize_kernel<__bf16, 1>, p, 1, stream)
+                                : moe::cast(moe::quantize_kernel<float, 1>, p, 1, stream);
 }
 
 moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int n_rows, int cols,
@@ -853,12 +883,10 @@ moe_status moe_dequantize_mxfp4(const uint8_t* codes, const uint8_t* scales, int
   if (s != MOE_OK || n_rows == 0) return s;
   moe::CastParams p{x, x_stride, const_cast<uint8_t*>(codes), const_cast<uint8_t*>(scales),
                     n_rows, 0, cols, 0, 0};
-  return moe::cast(p, [&](const moe::CastParams& q, dim3 grid) {
-    if (x_type == MOE_ACT_BF16)
-      hipLaunchKernelGGL((moe::dequantize_kernel<__bf16>), grid, dim3(moe::kThreads), 0, stream, q);
-    else
-      hipLaunchKernelGGL((moe::dequantize_kernel<float>), grid, dim3(moe::kThreads), 0, stream, q);
-  });
+  if (moe::large_cast(p, x_type))
+    return moe::cast(moe::dequantize_kernel<__bf16, true>, p, 1, stream);
+  return x_type == MOE_ACT_BF16 ? moe::cast(moe::dequantize_kernel<__bf16, false>, p, 1, stream)
+                                : moe::cast(moe::dequantize_kernel<float, false>, p, 1, stream);
 }
 
 moe_status moe_product_mxfp4(const moe_mxfp4_weight* w, const uint8_t* codes,

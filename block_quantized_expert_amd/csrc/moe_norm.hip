@@ -102,20 +102,6 @@ __device__ __forceinline__ float weight_at(const void* weight, int bf16, int c) 
               : static_cast<const float*>(weight)[c];
 }
 
-// Eight columns past the caches.  Of many rows the stores go there: lines that
-// stay would cost other lines' write-back (4096 x 4096 bf16, the residual added:
-// 31.3 us, y past the caches 28.8, the total as well 22.8; loads there 25.3;
-// gradients 30.5, dx past them 24.7).
-typedef uint32_t PastVec __attribute__((ext_vector_type(4), aligned(2)));
-template <typename T>
-__device__ __forceinline__ void store_past(T* p, const Cols8<T>& r) {
-  PastVec v[sizeof(r) / 16];
-  __builtin_memcpy(v, &r, sizeof(r));
-#pragma unroll
-  for (unsigned i = 0; i < sizeof(r) / 16; ++i)
-    __builtin_nontemporal_store(v[i], reinterpret_cast<PastVec*>(p) + i);
-}
-
 // Where a lane's eight columns lie that begin at `nominal`: rows have at least
 // eight columns, and the last lane takes the last eight, of which the first
 // `skip` belong to its neighbour; a lane past the row's end skips all of them.
@@ -126,6 +112,11 @@ struct Columns {
       : c(nominal + 8 <= hidden ? nominal : hidden - 8),
         skip(nominal + 8 <= hidden ? 0 : nominal < hidden ? nominal + 8 - hidden : 8) {}
 };
+// Of many rows the stores go past the caches (PAST): lines that stay would cost
+// other lines' write-back (4096 x 4096 bf16, the residual added: 31.3 us, y past
+// the caches 28.8, the total as well 22.8; loads there 25.3; gradients 30.5, dx
+// past them 24.7; the norm and a 4096 x 4096 product that reads it 130.4 and
+// 128.2).
 template <bool PAST, typename T>
 __device__ __forceinline__ void store_own(T* row, const Columns& at, const Cols8<T>& r) {
   if (at.skip == 0) {

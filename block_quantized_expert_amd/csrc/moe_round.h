@@ -58,6 +58,16 @@ __device__ __forceinline__ void store_cols(T* p, const Cols8<T>& r, int m) {
   for (int i = 0; i < 8; ++i)
     if (i < m) p[i] = r.v[i];
 }
+// Past the caches: for outputs too large to be found there by their reader.
+typedef uint32_t PastVec __attribute__((ext_vector_type(4), aligned(2)));
+template <typename T>
+__device__ __forceinline__ void store_past(T* p, const Cols8<T>& r) {
+  PastVec v[sizeof(r) / 16];
+  __builtin_memcpy(v, &r, sizeof(r));
+#pragma unroll
+  for (unsigned i = 0; i < sizeof(r) / 16; ++i)
+    __builtin_nontemporal_store(v[i], reinterpret_cast<PastVec*>(p) + i);
+}
 
 // ----------------------------------------------------------------- MXFP4
 
