@@ -36,7 +36,7 @@ EXPORTED = ["moe_route", "moe_route_hash", "moe_route_group", "moe_group_workspa
             "moe_int8_form", "moe_rmsnorm", "moe_rmsnorm_int8", "moe_rmsnorm_mxfp4",
             "moe_rmsnorm_backward", "moe_rmsnorm_backward_workspace_bytes",
             "moe_quantize_mxfp4", "moe_dequantize_mxfp4", "moe_product_mxfp4",
-            "moe_swiglu_mxfp4"]
+            "moe_swiglu_mxfp4", "moe_mxfp4_form"]
 
 WEIGHT_TYPES = {"mxfp4": MOE_W_MXFP4, "fp8_e4m3_b128": MOE_W_FP8E4M3_B128}
 
@@ -177,6 +177,7 @@ def lib() -> ctypes.CDLL:
                      "moe_product_int8", "moe_swiglu_int8", "moe_int8_form"):
             getattr(L, name).restype = ctypes.c_int
         R, M = ctypes.POINTER(MoeNormRows), ctypes.POINTER(MoeMxfp4Weight)
+        L.moe_mxfp4_form.argtypes = [I, I, I, I, I, I, N, N, N]
         L.moe_rmsnorm.argtypes = [R, P, I, D, P]
         L.moe_rmsnorm_int8.argtypes = [R, P, P, P]
         L.moe_rmsnorm_mxfp4.argtypes = [R, P, P, P]
@@ -189,7 +190,7 @@ def lib() -> ctypes.CDLL:
         L.moe_swiglu_mxfp4.argtypes = [M, M, P, P, I, P, P, I, P, I, D, P]
         for name in ("moe_rmsnorm", "moe_rmsnorm_int8", "moe_rmsnorm_mxfp4",
                      "moe_rmsnorm_backward", "moe_quantize_mxfp4", "moe_dequantize_mxfp4",
-                     "moe_product_mxfp4", "moe_swiglu_mxfp4"):
+                     "moe_product_mxfp4", "moe_swiglu_mxfp4", "moe_mxfp4_form"):
             getattr(L, name).restype = ctypes.c_int
         L.moe_status_string.argtypes = [ctypes.c_int]
         L.moe_status_string.restype = ctypes.c_char_p
@@ -797,3 +798,12 @@ def moe_swiglu_mxfp4(gate, up, codes, scales, grouping=None, top_k=0, out_dtype=
     """SwiGLU of the gate and up products; arguments as moe_product_mxfp4."""
     return _call("product_mxfp4", stream, gate.address, gate.codes, up.address, up.codes, codes,
                  scales, grouping, top_k, out_dtype, out)
+
+
+def moe_mxfp4_form(n_experts, rows, cols, n_slots, grouped, swiglu):
+    """(rows a tile, channels a tile, persistent workgroups or 0) of the kernel
+    form that an MXFP4 product of these sizes takes (moe_probe.h)."""
+    out = [ctypes.c_int32() for _ in range(3)]
+    _check(lib().moe_mxfp4_form(n_experts, rows, cols, n_slots, int(grouped), int(swiglu),
+                                *[ctypes.byref(v) for v in out]), "moe_mxfp4_form")
+    return tuple(v.value for v in out)

@@ -10,6 +10,7 @@
 #include "moe_grouped.h"
 #include "moe_mxfp4.h"
 #include "moe_ops_host.h"
+#include "moe_probe.h"
 #include "moe_round.h"
 
 namespace moe {
@@ -904,6 +905,34 @@ moe_status moe_swiglu_mxfp4(const moe_mxfp4_weight* gate, const moe_mxfp4_weight
   if (up == nullptr) return MOE_ERR_INVALID;
   return moe::product(gate, up, codes, scales, n_slots, offsets, perm, top_k, out, out_type,
                       out_stride, stream);
+}
+
+moe_status moe_mxfp4_form(int n_experts, int rows, int cols, int n_slots, int grouped, int swiglu,
+                          int32_t* tile_rows, int32_t* tile_channels, int32_t* workgroups) {
+  if (tile_rows == nullptr || tile_channels == nullptr || workgroups == nullptr ||
+      n_experts <= 0 || rows <= 0 || cols <= 0 || n_slots <= 0 || (!grouped && n_experts != 1))
+    return MOE_ERR_INVALID;
+  if (n_experts > MOE_MAX_EXPERTS || rows > MOE_MAX_DIM || cols > MOE_MAX_DIM || cols % 32 != 0 ||
+      n_slots > MOE_MAX_TOKENS * MOE_MAX_TOP_K)
+    return MOE_ERR_UNSUPPORTED;
+  moe::ProductParams p{};
+  p.n_experts = n_experts;
+  p.rows = rows;
+  p.cols = cols;
+  p.n_slots = n_slots;
+  p.offsets = grouped ? tile_rows : nullptr;  // looked at for null only
+  const moe::Form f = moe::choose_form(p, swiglu != 0);
+  if (f < moe::kDirect32) {
+    const moe::TiledCost& c = moe::kTiledCost[f];
+    *tile_rows = c.rows;
+    *tile_channels = swiglu ? c.ch / 2 : c.ch;
+    *workgroups = moe::kCus * c.per_cu;
+  } else {
+    *tile_rows = f == moe::kDirect32 ? 32 : 16;
+    *tile_channels = f == moe::kDirect32 && !swiglu ? 32 : 16;
+    *workgroups = 0;
+  }
+  return MOE_OK;
 }
 
 }  // extern "C"

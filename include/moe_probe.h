@@ -73,6 +73,10 @@ size_t moe_mfma_rate_out_floats(void);
  */
 moe_status moe_int8_form(int n_experts, int rows, int cols, int n_slots, int grouped, int swiglu,
                          int32_t* tile_rows, int32_t* tile_channels, int32_t* workgroups);
+/* The same of moe_product_mxfp4 and moe_swiglu_mxfp4.  (A left operand of more
+ * than 4 GiB of codes that is gathered takes a kernel for few rows.) */
+moe_status moe_mxfp4_form(int n_experts, int rows, int cols, int n_slots, int grouped, int swiglu,
+                          int32_t* tile_rows, int32_t* tile_channels, int32_t* workgroups);
 
 #ifdef __cplusplus
 }

@@ -291,3 +291,52 @@ def test_reference_gradients_are_the_differences():
         t = np.zeros(5)
         t[j] = d
         assert abs((loss(s, w + t) - loss(s, w - t)) / (2 * d) - dw[j]) < 1e-7
+
+
+@pytest.mark.parametrize("sizes,expected", [
+    ((0, 8, 32, 1, 1, 0), INV), ((1, 0, 32, 1, 1, 0), INV), ((1, 8, 0, 1, 1, 0), INV),
+    ((1, 8, 32, 0, 1, 0), INV), ((2, 8, 32, 1, 0, 0), INV), ((1025, 8, 32, 1, 1, 0), UNS),
+    ((1, 65537, 32, 1, 1, 0), UNS), ((1, 8, 48, 1, 1, 0), UNS), ((1, 8, 65568, 1, 1, 0), UNS),
+    ((1, 8, 32, (1 << 25) + 1, 1, 0), UNS)])
+def test_mxfp4_form_refuses(sizes, expected):
+    out = [ctypes.c_int32() for _ in range(3)]
+    assert B.lib().moe_mxfp4_form(*sizes, *[ctypes.byref(v) for v in out]) == expected
+
+
+def test_mxfp4_form_refuses_null():
+    v = ctypes.byref(ctypes.c_int32())
+    for null in range(3):
+        out = [None if i == null else v for i in range(3)]
+        assert B.lib().moe_mxfp4_form(1, 8, 32, 1, 1, 0, *out) == INV
+
+
+def test_gpu_cases_take_every_mxfp4_form():
+    """Cases of test_gpu_mxfp4_tiles.py take every form, plain and with SwiGLU,
+    dense and grouped, with a reduction of one step and of several; and every
+    tile shape with two tiles and more for each persistent workgroup, where it
+    is chosen for so many (dense, the small shapes are not)."""
+    import test_gpu_mxfp4_tiles as G
+
+    tiles = [(256, 256), (128, 256), (64, 256), (32, 256), (128, 128), (64, 64)]
+    reached, several = set(), set()
+
+    def look(kind, e, rows, cols, counts, slots):
+        for swiglu in (False, True):
+            r, c, workgroups = B.moe_mxfp4_form(e, rows, cols, slots, kind == "grouped", swiglu)
+            form = (r, c * 2 if swiglu else c) if workgroups else r
+            reached.add((kind, swiglu, form, cols <= 256))
+            items = sum(-(-int(n) // r) for n in counts) * -(-rows // c)
+            if workgroups and items >= 2 * workgroups:
+                several.add((kind, swiglu, form))
+
+    for n, rows, cols in G.DENSE:
+        look("dense", 1, rows, cols, [n], n)
+    for e, slots, rows, cols in G.GROUPED:
+        look("grouped", e, rows, cols, G.counts_of(e, slots), slots)
+    want = {(kind, swiglu, form, one) for kind in ("dense", "grouped") for swiglu in (False, True)
+            for form in tiles + [16, 32] for one in (False, True)}
+    assert reached == want, (want - reached, reached - want)
+    want = {("grouped", swiglu, form) for swiglu in (False, True) for form in tiles}
+    want |= {("dense", swiglu, form) for swiglu in (False, True)
+             for form in tiles[:2] + [(128, 128)]}
+    assert several >= want, want - several
