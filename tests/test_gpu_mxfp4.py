@@ -72,6 +72,17 @@ def test_rounding_is_exact_both_ways(n, c, pad, dtype):
     _check_quantize(x.to(dtype), pad)
 
 
+# so many bf16 columns that a wavefront takes several words
+@pytest.mark.parametrize("n,c,pad", [(8201, 1056, 0), (37700, 224, 1), (2051, 4128, 0),
+                                     (263001, 32, 0), (129, 65536, 3)])
+def test_rounding_of_many_rows(n, c, pad):
+    print("case quantize many", n, c, pad, flush=True)
+    x = normal(n + c, n, c)
+    x[:, ::97] *= 12
+    x[n // 2, 5] = float("inf")
+    _check_quantize(x.bfloat16(), pad)
+
+
 def test_borders_and_far_values():
     # the borders of E2M1 under every scale, their neighbours in fp32, and what saturates
     borders = [0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0]
@@ -387,6 +398,23 @@ def test_a_layer_of_the_calls_together():
         total.double().cpu().numpy())
     errs = sum(tw64[:, i:i + 1] * err[inv[:, i]] for i in range(k)) + (k + 2) * U32 * mags
     assert_within(y, want, errs + half_step(BF16) * (np.abs(want) + errs), "y")
+
+
+def test_two_streams_at_once():
+    # the same weights and left operands on two streams, in turns without a wait
+    n, k, e, rows, cols = 64, 4, 16, 320, 1056
+    g = on_gpu(group(make_ids(n, k, e, 0.1, seed=2), e))
+    gate, up = (_gpu_weight(_weight(i, e, rows, cols)) for i in (1, 2))
+    x = _gpu_left(_left(3, n, cols))
+    want = B.moe_swiglu_mxfp4(gate, up, *x, g, top_k=k), B.moe_product_mxfp4(gate, *x, g, top_k=k)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for _ in range(4):
+        got += [(B.moe_swiglu_mxfp4(gate, up, *x, g, top_k=k, stream=s),
+                 B.moe_product_mxfp4(gate, *x, g, top_k=k, stream=s)) for s in streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for pair in got for a, b in zip(pair, want))
 
 
 def test_no_slots():

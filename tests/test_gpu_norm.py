@@ -8,8 +8,8 @@ bf16.  dx = rf (w dy) - k s + dtotal in fp32: three roundings in the first
 term, in the second one of k and one of the product beside the rounding of
 each w dy in k's sum, one for each of the two sums, then the output's.
 dweight: two products and the rounding of r a term, one rounding for each row
-that a workgroup adds and three more where wavefronts are joined, fp64 over
-the workgroups, one last rounding."""
+that a wavefront adds, of the workgroup's part one, fp64 over the wavefronts
+and the workgroups, one last rounding."""
 
 import numpy as np
 import pytest
@@ -78,6 +78,40 @@ def test_norm(n, h, pad, xt, rt, wt, yt):
         assert got is y
     ref, _ = norm_ref(f64(s), f64(w), EPS)
     assert_within(y, ref, _y_bound(ref, yt), "y")
+
+
+# so many rows that workgroups take several, one to four wavefronts a row
+MANY = [(5300, 513, 0), (6001, 520, 1), (1301, 2047, 0), (1282, 2048, 3), (1290, 2049, 0),
+        (1400, 2059, 1), (700, 4095, 0), (641, 4096, 0), (650, 4097, 5), (330, 8191, 1),
+        (321, 8192, 0), (2051, 1031, 0)]
+
+
+@pytest.mark.parametrize("xt,rt,wt,yt", [
+    (BF16, None, F32, BF16), (F32, None, BF16, F32), (BF16, BF16, BF16, BF16),
+    (F32, F32, F32, F32), (F32, BF16, F32, BF16), (BF16, F32, F32, F32)])
+@pytest.mark.parametrize("n,h,pad", MANY)
+def test_norm_of_many_rows(n, h, pad, xt, rt, wt, yt):
+    test_norm(n, h, pad, xt, rt, wt, yt)
+
+
+@pytest.mark.parametrize("xt,rt,wt", [(BF16, None, F32), (F32, F32, BF16), (F32, BF16, F32),
+                                      (BF16, BF16, BF16)])
+@pytest.mark.parametrize("n,h,pad", [(2600, 1024, 0), (5100, 544, 1), (1300, 2080, 0),
+                                     (700, 4064, 3), (650, 4128, 0), (330, 8160, 0)])
+def test_rounded_outputs_of_many_rows(n, h, pad, xt, rt, wt):
+    test_rounded_outputs_are_the_quantizers_on_the_fp32_output(n, h, pad, xt, rt, wt)
+
+
+@pytest.mark.parametrize("n,h", [(3, 5), (4, 513), (9, 1001), (5, 8201), (700, 4097), (5300, 519),
+                                 (1400, 2053)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_total_may_be_the_residual_at_odd_sizes(n, h, dtype):
+    x, res, w = (t.cuda() for t in _inputs(n, h, dtype, dtype, F32, h))
+    want = B.moe_rmsnorm(x, w, EPS, residual=res)
+    assert torch.equal(want[1], (x.float() + res.float()).to(dtype))
+    r = strided(res, 3).clone() if n < 10 else res.clone()
+    y, total = B.moe_rmsnorm(x, w, EPS, residual=r, total=r)
+    assert total is r and torch.equal(r, want[1]) and torch.equal(y, want[0])
 
 
 @pytest.mark.parametrize("xt,rt,wt", [(BF16, None, F32), (F32, F32, BF16), (F32, BF16, F32),
@@ -231,6 +265,51 @@ def test_gradients(n, h, pad, dt, st, wt, total):
     _back_check(n, h, pad, dt, st, wt, total)
 
 
+# rows by the thousand: one to sixteen wavefronts a row, several rows at once
+@pytest.mark.parametrize("dt,st,wt,total", [
+    (BF16, BF16, F32, True), (F32, F32, F32, False), (BF16, F32, BF16, True),
+    (BF16, BF16, BF16, False), (F32, F32, BF16, True)])
+@pytest.mark.parametrize("n,h,pad", [(1537, 513, 0), (1600, 1031, 1), (1701, 2053, 0),
+                                     (1541, 4099, 0), (1600, 8191, 0), (4200, 1024, 0),
+                                     (5003, 9, 1), (520, 517, 0), (1536, 1025, 0)])
+def test_gradients_of_many_rows(n, h, pad, dt, st, wt, total):
+    print("case gradients", n, h, pad, dt, st, wt, total, flush=True)
+    _back_check(n, h, pad, dt, st, wt, total)
+
+
+@pytest.mark.parametrize("n,h", [(3, 5), (9, 1001), (5, 8201), (1600, 1025), (1601, 4097)])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_gradients_into_dtotal_at_odd_sizes(n, h, dtype):
+    s, _, w = (t if t is None else t.cuda() for t in _inputs(n, h, dtype, None, F32, h))
+    dy, tot = normal(1, n, h, dtype=dtype).cuda(), normal(2, n, h, dtype=dtype).cuda()
+    dx, dw = B.moe_rmsnorm_backward(dy, s, w, EPS, dtotal=tot)
+    got = B.moe_rmsnorm_backward(dy, s, w, EPS, dtotal=tot, dx=tot)
+    assert got[0] is tot and torch.equal(tot, dx) and torch.equal(got[1], dw)
+
+
+def test_short_rows_of_more_than_a_launch():
+    # rows of fewer than eight columns go in launches of 2^21, with their gradients
+    n, h = (1 << 21) + 5, 3
+    x = torch.arange(n * h, device="cuda").remainder(13).sub(6).float().view(n, h)
+    x[:, 0] += 0.5
+    w = torch.tensor([1.0, 0.5, 2.0], device="cuda")
+    y = B.moe_rmsnorm(x, w, EPS)
+    at = [0, 1, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, n - 1]
+    ref, _ = norm_ref(f64(x[at]), f64(w), EPS)
+    assert_within(y[at], ref, _y_bound(ref, F32), "y")
+    total = torch.empty_like(x)
+    y2, t2 = B.moe_rmsnorm(x, w, EPS, residual=torch.zeros_like(x), total=total)
+    assert t2 is total and torch.equal(total, x) and torch.equal(y2, y)
+    dx, dw = B.moe_rmsnorm_backward(x, x, w, EPS)
+    want, _ = norm_back_ref(f64(x[at]), f64(x[at]), f64(w), EPS)
+    # each of dx's terms is below 2^5 and rounded four times
+    assert_within(dx[at], want, 4 * U32 * 2.0 ** 5, "dx")
+    _, dwr = norm_back_ref(f64(x), f64(x), f64(w), EPS)
+    rows = -(-n // 64) + 1
+    assert_within(dw, dwr, U32 * (6 + rows) * (f64(x) ** 2 * norm_ref(f64(x), 1.0, EPS)[1]).sum(0),
+                  "dweight")
+
+
 def test_gradients_against_differences():
     # L = sum(dy * n(x)) in 64 bits; a central difference of step d is off by
     # d^2 / 6 times the third derivative (of order 1 here) and 2^-53 L / d: with
@@ -334,6 +413,22 @@ def test_results_repeat_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want)), i
+
+
+def test_gradients_on_two_streams_at_once():
+    # each call has a workspace of its own
+    n, h = 3001, 1031
+    s, _, w = (t if t is None else t.cuda() for t in _inputs(n, h, BF16, None, F32, 1))
+    dys = [normal(9 + i, n, h, dtype=BF16).cuda() for i in range(2)]
+    want = [B.moe_rmsnorm_backward(dy, s, w, EPS) for dy in dys]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[B.moe_rmsnorm_backward(dy, s, w, EPS, stream=st) for dy, st in zip(dys, streams)]
+           for _ in range(4)]
+    torch.cuda.synchronize()
+    for both in got:
+        for a, b in zip(both, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
 def test_refusals_on_the_gpu():
