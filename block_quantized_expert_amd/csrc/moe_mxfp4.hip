@@ -726,9 +726,13 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
 
 // The kernels' forms, and what a product takes with each, in microseconds:
 // least squares on the logarithms of every form's times over dense and grouped
-// products of 1 to 24576 rows, without the rounding of the left operand.  To be
-// fitted anew when a form's kernel changes.
-enum Form { k256x256, k128x256, k64x256, k32x256, k128x128, k64x64, kDirect32, kDirect16 };
+// products of 1 to 24576 rows, without the rounding of the left operand; the
+// chosen form takes 1.2 % more than the best of the 146 cases' forms on average
+// and 32 % at most, where far fewer experts than slots have rows.  To be fitted
+// anew when a form's kernel changes.
+enum Form {
+  k256x256, k128x256, k64x256, k32x256, k128x128, k64x64, kDirect32, kDirect32x16, kDirect16
+};
 struct TiledCost {
   int rows, ch;             // tile (SwiGLU: of ch / 2 channels)
   int per_cu;               // workgroups on a CU
@@ -737,9 +741,22 @@ struct TiledCost {
                             // of it where the weights come from HBM, and once
 };
 constexpr TiledCost kTiledCost[kDirect32] = {
-    {256, 256, 1, 9.8, 1.63, 0.86, 0.9}, {128, 256, 1, 6.4, 0.99, 0.39, 1.8},
-    {64, 256, 1, 4.8, 0.78, 0.33, 2.1},  {32, 256, 1, 4.6, 0.67, 0.40, 1.8},
-    {128, 128, 1, 6.1, 0.64, 0.16, 1.0}, {64, 64, 2, 4.4, 0.43, 0.23, 1.6}};
+    {256, 256, 1, 8.5, 1.62, 0.90, 1.1}, {128, 256, 1, 5.3, 0.95, 0.41, 2.2},
+    {64, 256, 1, 3.9, 0.76, 0.33, 2.5},  {32, 256, 1, 3.4, 0.61, 0.43, 2.3},
+    {128, 128, 1, 4.8, 0.60, 0.18, 1.4}, {64, 64, 2, 2.5, 0.40, 0.22, 2.1}};
+// The direct forms: the launch and the look-up of a tile, the latency of a
+// reduction by its length, both operands' bytes (every workgroup reads its own)
+// at a rate of L2 that weights from HBM divide by about two, and a workgroup's
+// start; a CU without a workgroup takes as long as the others.
+struct DirectCost {
+  int rows, strip, swiglu_strip;
+  double start, input;  // us, and for each input of a row
+  double rate, cold;    // bytes a us, its divisor where the weights come from HBM
+  double group;
+};
+constexpr DirectCost kDirectCost[] = {{32, 32, 16, 1.9, 0.23e-3, 11.6e6, 2.1, 5.3e-3},
+                                      {32, 16, 0, 2.2, 0.21e-3, 14.4e6, 2.2, 3.1e-3},
+                                      {16, 16, 16, 2.4, 0.05e-3, 12.3e6, 2.0, 2.3e-3}};
 
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) {
@@ -762,19 +779,20 @@ Form choose_form(const ProductParams& p, bool swiglu) {
   const bool cold = live * p.rows * row_bytes * (swiglu ? 2 : 1) > 256e6;
   const double mean = (double)p.n_slots / p.n_experts;
   Form best = kDirect16;
-  double least = 0;
-  // The direct forms: the launch and the look-up of a tile, the latency of a
-  // reduction by its length, both operands' bytes (every workgroup reads its
-  // own) at a rate of L2 that weights from HBM divide by about two, and a
-  // workgroup's start.
-  for (int wide = 0; wide < 2; ++wide) {
-    const int tm = wide ? 32 : 16, strip = wide && !swiglu ? 32 : 16;
-    const double groups = expected_tiles(p, tm) * ((p.rows + strip - 1) / strip);
-    const double bytes = groups * row_bytes * ((swiglu ? 32 : strip) + (mean < tm ? mean : tm));
-    const double us = wide ? 3.1 + p.cols * 0.36e-3 + bytes * (cold ? 1.86 : 1) / 9.6e6 + groups * 4.1e-3
-                           : 2.9 + bytes * (cold ? 1.66 : 1) / 9.9e6 + groups * 2.1e-3;
-    if (!wide || us < least) {
-      best = wide ? kDirect32 : kDirect16;
+  double least = HUGE_VAL;
+  for (int f = kDirect32; f <= kDirect16; ++f) {
+    const DirectCost& c = kDirectCost[f - kDirect32];
+    const int strip = swiglu ? c.swiglu_strip : c.strip;
+    if (strip == 0) continue;
+    double rounds = expected_tiles(p, c.rows) * ((p.rows + strip - 1) / strip) / kCus;
+    rounds = p.offsets == nullptr ? ceil(rounds) : rounds > 1 ? rounds : 1.0;
+    const double groups = rounds * kCus;
+    const double bytes =
+        groups * row_bytes * ((swiglu ? 2 * strip : strip) + (mean < c.rows ? mean : c.rows));
+    const double us =
+        c.start + p.cols * c.input + bytes * (cold ? c.cold : 1) / c.rate + groups * c.group;
+    if (us < least) {
+      best = (Form)f;
       least = us;
     }
   }
@@ -822,6 +840,9 @@ hipError_t launch_product(const ProductParams& p, hipStream_t stream) {
     case k128x128: return launch_tiled<SWIGLU, O, 128, 128, 2, 4, 4>(p, 1, stream);
     case k64x64: return launch_tiled<SWIGLU, O, 64, 64, 2, 2, 4>(p, 2, stream);
     case kDirect32: launch_direct<SWIGLU, O, 2, SWIGLU ? 1 : 2>(p, stream); break;
+    case kDirect32x16:  // plain products only
+      if constexpr (!SWIGLU) launch_direct<SWIGLU, O, 2, 1>(p, stream);
+      break;
     default: launch_direct<SWIGLU, O, 1, 1>(p, stream);
   }
   return hipGetLastError();
@@ -928,8 +949,9 @@ moe_status moe_mxfp4_form(int n_experts, int rows, int cols, int n_slots, int gr
     *tile_channels = swiglu ? c.ch / 2 : c.ch;
     *workgroups = moe::kCus * c.per_cu;
   } else {
-    *tile_rows = f == moe::kDirect32 ? 32 : 16;
-    *tile_channels = f == moe::kDirect32 && !swiglu ? 32 : 16;
+    const moe::DirectCost& c = moe::kDirectCost[f - moe::kDirect32];
+    *tile_rows = c.rows;
+    *tile_channels = swiglu ? c.swiglu_strip : c.strip;
     *workgroups = 0;
   }
   return MOE_OK;

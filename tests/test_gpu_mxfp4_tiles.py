@@ -23,6 +23,8 @@ DENSE = [
     (513, 6837, 288), (6742, 259, 32), (396, 8953, 544), (1936, 8193, 288), (901, 8871, 800),
     (3897, 4083, 672), (1946, 3985, 64), (7976, 3997, 32), (6559, 4867, 288), (2850, 3524, 288),
     (4017, 3999, 32), (2865, 7042, 288), (2570, 6301, 832), (5038, 6623, 544),
+    (306, 193, 288), (17, 2120, 32), (37, 2074, 576), (408, 8280, 64), (5696, 324, 544),
+    (6758, 1155, 32), (1836, 4376, 544),
 ]
 # experts, slots, weight rows, cols
 GROUPED = [
@@ -37,7 +39,10 @@ GROUPED = [
     (256, 5889, 656, 608), (150, 7364, 283, 384), (3, 4013, 2108, 544), (150, 7473, 279, 608),
     (40, 1964, 4613, 576), (256, 6960, 1063, 32), (1, 7054, 4613, 576), (5, 4632, 7185, 32),
     (150, 6954, 1032, 320), (1, 5890, 5643, 288), (5, 4744, 3548, 544), (1024, 7900, 300, 544),
-    (1024, 2001, 211, 160),
+    (1024, 2001, 211, 160), (3, 54, 1290, 32), (5, 546, 123, 288), (1, 608, 128, 544),
+    (64, 2897, 3107, 288), (256, 5805, 209, 544), (40, 3094, 656, 544), (150, 6739, 1161, 32),
+    (150, 6641, 1066, 544), (40, 3515, 4843, 32), (1, 7469, 1048, 800), (40, 3608, 4700, 288),
+    (64, 5763, 2888, 608),
 ]
 
 

@@ -318,12 +318,13 @@ def test_gpu_cases_take_every_mxfp4_form():
     import test_gpu_mxfp4_tiles as G
 
     tiles = [(256, 256), (128, 256), (64, 256), (32, 256), (128, 128), (64, 64)]
+    few = {False: [(16, 16), (32, 16), (32, 32)], True: [(16, 32), (32, 32)]}
     reached, several = set(), set()
 
     def look(kind, e, rows, cols, counts, slots):
         for swiglu in (False, True):
             r, c, workgroups = B.moe_mxfp4_form(e, rows, cols, slots, kind == "grouped", swiglu)
-            form = (r, c * 2 if swiglu else c) if workgroups else r
+            form = (r, c * 2 if swiglu else c)
             reached.add((kind, swiglu, form, cols <= 256))
             items = sum(-(-int(n) // r) for n in counts) * -(-rows // c)
             if workgroups and items >= 2 * workgroups:
@@ -334,7 +335,7 @@ def test_gpu_cases_take_every_mxfp4_form():
     for e, slots, rows, cols in G.GROUPED:
         look("grouped", e, rows, cols, G.counts_of(e, slots), slots)
     want = {(kind, swiglu, form, one) for kind in ("dense", "grouped") for swiglu in (False, True)
-            for form in tiles + [16, 32] for one in (False, True)}
+            for form in tiles + few[swiglu] for one in (False, True)}
     assert reached == want, (want - reached, reached - want)
     want = {("grouped", swiglu, form) for swiglu in (False, True) for form in tiles}
     want |= {("dense", swiglu, form) for swiglu in (False, True)
