@@ -112,9 +112,6 @@ double expected_tiles(const GroupedRows& p, int tm) {
 
 typedef __attribute__((address_space(4))) const int32_t* scalar_i32;
 
-// Sixteen bytes that a copy past the end of a row reads instead.
-__device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
-
 constexpr int kTableSpan = MOE_MAX_EXPERTS / kWave + 1;
 constexpr int kCus = 256;
 

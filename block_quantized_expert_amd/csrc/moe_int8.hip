@@ -224,6 +224,9 @@ __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams 
 
 // ------------------------------------------------------------- tiled products
 
+// Sixteen bytes that a copy past the end of a row reads instead.
+__device__ const u32x4 kZeroChunk = {0, 0, 0, 0};
+
 // LDS: STAGES steps of weights [CH][128] and rows [TOK][128], then kSlots
 // tiles' scales (of the CH weight rows, and of the rows eight times each, as
 // the copies place them), then the tiles in front of each expert's.  A tile's

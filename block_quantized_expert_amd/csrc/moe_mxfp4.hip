@@ -186,7 +186,14 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));  // scale bytes of 2
 // operands straight from memory into the matrix instruction, partial sums
 // joined in LDS.  Nothing is shared that a few rows could not load again, so
 // the only waits are for memory: each wavefront has up to 4 turns' loads in
-// flight.
+// flight.  Bound by the launch and one trip to memory where the weights are in
+// the caches (1 x 4096 x 4096 3.9 us, an empty launch 2.5), by HBM where they
+// are not (one token through six of 256 experts' gate and up of 2048 x 4096,
+// 53 MB, 12.9 us, 4.2 TB/s).  32 x 16 tiles read a weight once for up to 32
+// rows with a workgroup on every CU (32 x 4096 x 4096 5.6 us; 16 x 16 6.4, 32 x
+// 32 7.3), 32 x 32 halve the reads of rows where there are channels enough (24
+// x 2048 x 7168 4.7, 5.4, 6.2 of 16 x 16).  A wavefront that loaded all weights
+// of a turn before its rows took 180 registers and 17.3 us for the one token.
 template <bool SWIGLU, typename O, int PER, int TB, int CB>
 __global__ __launch_bounds__(kThreads) void product_direct_kernel(ProductParams p) {
   static_assert(!SWIGLU || CB == 1, "blocks");
@@ -380,6 +387,25 @@ __device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
 // to tile never waits for a first load; LDS also turns whole 128-byte lines of
 // memory into the matrix instruction's layout.  A word of scales serves two
 // steps of a row, and a wavefront copies those of all its rows at once.
+//
+// What bounds it: for 4096 x 4096 x 4096 (38 us, 3.6 PFLOP/s) the card's power,
+// which takes the clock down to 2.0 GHz while the matrix cores are busy half
+// the time (codes that are all zero take three quarters of the time); for
+// experts' weights of 2.3 GB HBM (256 experts' gate and up of 2048 x 4096: 357
+// us for 512 tokens, 6.4 TB/s), and for 4096 tokens, 96 rows an expert, both
+// (475 us, 4.8 TB/s and 1.7 PFLOP/s).
+//   - Copies between the products, one every unit or two, not all in front: a
+//     wavefront waits at a copy's issue while the CU has many lines in flight.
+//   - Three stages of 128 x 256 tiles, four of the smaller ones, are as many as
+//     LDS holds; 256 x 256 tiles hold two and are for long dense products.
+//   - A step is one block of straight code: the compiler moves products past
+//     any branch behind them, and keeps sums in memory to do so.
+//   - The last part writes 64 or 128 whole bytes a token, which neighbouring
+//     lanes hold after up to three exchanges.  (With this, the third stage and
+//     the copies as buffer loads 4096 tokens' gate and up went from 610 to 485
+//     us, their down projection from 375 to 265.)
+//   - Weights in the order of the copies, a tile's step in one piece, gained
+//     nothing over rows as they are.
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductParams p) {
   constexpr int NW = WT * WC;
@@ -431,7 +457,10 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
   const int chunk_even = (lane % 8) ^ (lane / 16);  // rows 8j + lane / 8 of even j
   int load_step = 0, into = 0, scale_into = 0;
   bool scales_due = false;
-  // an expert's only tile, whose weights are read once
+  // an expert's only tile: its weights are read once and go past the caches (512
+  // tokens' gate and up 398 -> 357 us; another tile of the expert would miss
+  // them there).  Taller tiles are chosen for experts of several, and two
+  // bodies of their step cost more than this gains.
   constexpr bool kOnce = TB == 1 && CH == 256;
   bool load_only = false;
   auto x_copy = [&](int i) { return (wave * kX + i) % (TOK / 8); };
@@ -451,7 +480,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     for (int i = 0; i < kW; ++i) {
       const int j = wave * kW + i;
       woffset[i] =
-          (uint32_t)channel(8 * j + lane / 8, it.j0) * row_bytes + 16 * (chunk_even ^ (4 * (j & 1)));
+          (uint32_t)channel(8 * j + lane / 8, it.j0) * row_bytes +
+          16 * (chunk_even ^ (4 * (j & 1)));
     }
     wsoffset = 16 * channel(wave * 8 * kW + lane % (SWIGLU ? 16 : 8 * kW), it.j0);
     xsbase = p.x_scales;
@@ -573,7 +603,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
       wv[h % kWRing][c] = *reinterpret_cast<const u32x4*>(buf + (woff ^ (16 * h)) + c * 4096);
   };
   auto read_x = [&](const char* buf, int u) {
-    xv[u % 4] = *reinterpret_cast<const u32x4*>(buf + (xoff ^ (16 * (u / TB))) + u % TB * WT * 4096);
+    xv[u % 4] =
+        *reinterpret_cast<const u32x4*>(buf + (xoff ^ (16 * (u / TB))) + u % TB * WT * 4096);
   };
   int from = STAGES - 1, scale_from = L::kSlots - 1;
   // the next step's copies have landed, and every wavefront has read this
@@ -586,7 +617,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
     from = from + 1 == STAGES ? 0 : from + 1;
     if (step % 2 == 0) scale_from = scale_from + 1 == L::kSlots ? 0 : scale_from + 1;
     const char* const buf = smem + from * L::kStage;
-    // eight bytes a lane: reads of four would meet on a quarter of the banks (8 cycles each, these 4)
+    // eight bytes a lane: reads of four would meet on a quarter of the banks (8 cycles each,
+    // these 4)
     const char* const scales = smem + L::kScales + scale_from * L::kSlot + step % 2 * 8;
 #pragma unroll
     for (int c = 0; c < CB; ++c)
@@ -681,7 +713,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
 #pragma unroll
       for (int i = 0; i < kPieces; i += G) {
         // G pieces of a lane change hands with the tokens 16 and 8 lanes on, so that a store
-        // writes 32 G whole bytes of each of its tokens (see the kernel's comment)
+        // writes 32 G whole bytes of each of its tokens
         if constexpr (G >= 2)
 #pragma unroll
           for (int k = 0; k < G / 2; ++k)
@@ -703,7 +735,8 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
           O* const out = static_cast<O*>(p.out) + (it.row0 + (int64_t)tok) * p.out_stride + j;
           if (tok >= it.m) continue;
           if (j + 4 * N <= p.rows) {
-            // grouped outputs past the caches, which the weights go through
+            // past the caches, which the operands go through (4096 x 4096 x 4096 40.0 ->
+            // 39.3 us)
             if (past)
               __builtin_nontemporal_store(
                   u32x4{piece[i + k][0], piece[i + k][1], piece[i + k][2], piece[i + k][3]},
