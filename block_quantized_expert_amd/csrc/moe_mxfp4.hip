@@ -780,16 +780,17 @@ constexpr TiledCost kTiledCost[kDirect32] = {
 // The direct forms: the launch and the look-up of a tile, the latency of a
 // reduction by its length, both operands' bytes (every workgroup reads its own)
 // at a rate of L2 that weights from HBM divide by about two, and a workgroup's
-// start; a CU without a workgroup takes as long as the others.
+// start; a CU without a workgroup takes as long as the others, one with fewer
+// (known of a dense product) half of the difference.
 struct DirectCost {
   int rows, strip, swiglu_strip;
   double start, input;  // us, and for each input of a row
   double rate, cold;    // bytes a us, its divisor where the weights come from HBM
   double group;
 };
-constexpr DirectCost kDirectCost[] = {{32, 32, 16, 1.9, 0.23e-3, 11.6e6, 2.1, 5.3e-3},
-                                      {32, 16, 0, 2.2, 0.21e-3, 14.4e6, 2.2, 3.1e-3},
-                                      {16, 16, 16, 2.4, 0.05e-3, 12.3e6, 2.0, 2.3e-3}};
+constexpr DirectCost kDirectCost[] = {{32, 32, 16, 1.8, 0.19e-3, 11.0e6, 1.9, 5.5e-3},
+                                      {32, 16, 0, 2.2, 0.19e-3, 13.6e6, 2.1, 3.2e-3},
+                                      {16, 16, 16, 2.4, 0.04e-3, 11.9e6, 2.0, 2.3e-3}};
 
 template <bool SWIGLU, typename O, int TOK, int CH, int WT, int WC, int STAGES>
 hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) {
@@ -818,7 +819,8 @@ Form choose_form(const ProductParams& p, bool swiglu) {
     const int strip = swiglu ? c.swiglu_strip : c.strip;
     if (strip == 0) continue;
     double rounds = expected_tiles(p, c.rows) * ((p.rows + strip - 1) / strip) / kCus;
-    rounds = p.offsets == nullptr ? ceil(rounds) : rounds > 1 ? rounds : 1.0;
+    if (p.offsets == nullptr) rounds = (rounds + ceil(rounds)) / 2;
+    if (rounds < 1) rounds = 1;
     const double groups = rounds * kCus;
     const double bytes =
         groups * row_bytes * ((swiglu ? 2 * strip : strip) + (mean < c.rows ? mean : c.rows));

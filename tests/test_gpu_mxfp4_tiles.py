@@ -42,7 +42,7 @@ GROUPED = [
     (1024, 2001, 211, 160), (3, 54, 1290, 32), (5, 546, 123, 288), (1, 608, 128, 544),
     (64, 2897, 3107, 288), (256, 5805, 209, 544), (40, 3094, 656, 544), (150, 6739, 1161, 32),
     (150, 6641, 1066, 544), (40, 3515, 4843, 32), (1, 7469, 1048, 800), (40, 3608, 4700, 288),
-    (64, 5763, 2888, 608),
+    (64, 5763, 2888, 608), (1, 611, 115, 320), (1, 764, 102, 576),
 ]
 
 
