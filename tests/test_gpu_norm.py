@@ -83,7 +83,7 @@ def test_norm(n, h, pad, xt, rt, wt, yt):
 # so many rows that workgroups take several, one to four wavefronts a row
 MANY = [(5300, 513, 0), (6001, 520, 1), (1301, 2047, 0), (1282, 2048, 3), (1290, 2049, 0),
         (1400, 2059, 1), (700, 4095, 0), (641, 4096, 0), (650, 4097, 5), (330, 8191, 1),
-        (321, 8192, 0), (2051, 1031, 0)]
+        (321, 8192, 0), (2051, 1031, 0), (400, 5003, 0), (260, 8189, 0)]
 
 
 @pytest.mark.parametrize("xt,rt,wt,yt", [
@@ -271,7 +271,8 @@ def test_gradients(n, h, pad, dt, st, wt, total):
     (BF16, BF16, BF16, False), (F32, F32, BF16, True)])
 @pytest.mark.parametrize("n,h,pad", [(1537, 513, 0), (1600, 1031, 1), (1701, 2053, 0),
                                      (1541, 4099, 0), (1600, 8191, 0), (4200, 1024, 0),
-                                     (5003, 9, 1), (520, 517, 0), (1536, 1025, 0)])
+                                     (5003, 9, 1), (520, 517, 0), (1536, 1025, 0),
+                                     (1801, 5119, 0), (1702, 5123, 1), (1600, 6200, 0)])
 def test_gradients_of_many_rows(n, h, pad, dt, st, wt, total):
     print("case gradients", n, h, pad, dt, st, wt, total, flush=True)
     _back_check(n, h, pad, dt, st, wt, total)
