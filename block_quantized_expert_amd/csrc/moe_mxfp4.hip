@@ -74,13 +74,8 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(CastParams p) {
     }
     const uint32_t byte = mxfp4_byte(block_max(top));
     const uint32_t codes = mxfp4_codes(v, byte);
-    auto* const to = reinterpret_cast<uint32_t*>(p.codes + at[u].row * (p.cols / 2) + at[u].c / 2);
-    if (at[u].in) {
-      if (U > 1)
-        __builtin_nontemporal_store(codes, to);
-      else
-        *to = codes;
-    }
+    if (at[u].in)
+      *reinterpret_cast<uint32_t*>(p.codes + at[u].row * (p.cols / 2) + at[u].c / 2) = codes;
     // lane i < 4 of a row stores bytes 4i .. 4i + 3 of the row's word, which its
     // lanes 16i, 16i + 4, ... hold; past the row's end they are 0
     uint32_t word = 0;
@@ -119,11 +114,14 @@ __global__ __launch_bounds__(kThreads) void dequantize_kernel(CastParams p) {
 }
 
 // Large casts of bf16 rows (us, 4096 and 8192 rows of 4096): to MXFP4 a
-// wavefront takes four words, their loads at once and the codes past the caches
-// (10.5 -> 9.5, 20.4 -> 17.4; 2048 rows 6.7 -> 6.3, 1024 rows 4.5 -> 4.7); back,
-// the rows go past the caches (9.6 -> 8.3, 19.9 -> 14.2; 2048 rows 6.5 -> 5.4).
-// fp32 rows gain nothing (4096 rows to MXFP4 15.6 and 15.0) or lose: a lane's 32
-// bytes are two stores, and half lines past the caches take 23 us, not 19.
+// wavefront takes four words, their loads at once (10.5 -> 9.9, 20.4 -> 18.8; 2048
+// rows 6.7 -> 6.5, 1024 rows 4.5 -> 4.8); back, the rows go past the caches (9.6 ->
+// 8.3, 19.9 -> 14.2; 2048 rows 6.5 -> 5.4).  Codes past the caches are written
+// sooner (9.5, 17.4), but whoever reads them waits longer: both casts one after
+// the other 20.6 and 35.6 where 18.3 and 31.0, with a product of 4096 channels
+// 54.2 and 94.3 where 52.3 and 91.1.  fp32 rows gain nothing (4096 rows to MXFP4
+// 15.6 and 15.0) or lose: a lane's 32 bytes are two stores, and half lines past
+// the caches take 23 us, not 19.
 constexpr int kCastUnits = 4;
 bool large_cast(const CastParams& p, int type) {
   return type == MOE_ACT_BF16 && p.n_rows * p.cols >= 1 << 23;

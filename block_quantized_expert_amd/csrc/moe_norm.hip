@@ -119,7 +119,8 @@ struct Columns {
 // other lines' write-back (4096 x 4096 bf16, the residual added: 31.3 us, y past
 // the caches 28.8, the total as well 22.8; loads there 25.3; gradients 30.5, dx
 // past them 24.7; the norm and a 4096 x 4096 product that reads it 130.4 and
-// 128.2).
+// 128.2).  Codes and q do not: a product that reads them at once gains what their
+// stores cost (8192 x 4096 to MXFP4 and 4096 channels 127.0 us past, 123.9).
 template <bool PAST, typename T>
 __device__ __forceinline__ void store_own(T* row, const Columns& at, const Cols8<T>& r) {
   if (at.skip == 0) {
@@ -137,7 +138,6 @@ __device__ __forceinline__ void store_own(T* row, const Columns& at, const Cols8
 // A row's eight rounded values: codes and the scale byte of each block.  Every
 // lane of the wavefront calls this; its columns are one word of scales, the
 // word's padding included.
-template <bool PAST>
 __device__ __forceinline__ void store_mxfp4(const NormParams& p, int64_t row, int c,
                                             const float (&n)[8]) {
   uint32_t m = 0;
@@ -149,15 +149,10 @@ __device__ __forceinline__ void store_mxfp4(const NormParams& p, int64_t row, in
         c < p.hidden ? byte : 0;
   if (c < p.hidden) {
     const uint32_t codes = mxfp4_codes(n, byte);
-    auto* const to =
-        reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * (p.hidden / 2) + c / 2);
-    if (PAST)
-      __builtin_nontemporal_store(codes, to);
-    else
-      *to = codes;
+    *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.y) + row * (p.hidden / 2) + c / 2) =
+        codes;
   }
 }
-template <bool PAST>
 __device__ __forceinline__ void store_int8(const NormParams& p, int64_t row, int c,
                                            const float (&n)[8], uint32_t top) {
   const float a = __uint_as_float(top), inv = 127.0f / a;
@@ -178,12 +173,7 @@ __device__ __forceinline__ void store_int8(const NormParams& p, int64_t row, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[i / 4] |= (uint32_t)((int)q[i] & 0xFF) << (8 * (i % 4));
   }
-  typedef uint32_t Word2 __attribute__((ext_vector_type(2)));
-  auto* const to = reinterpret_cast<Word2*>(static_cast<int8_t*>(p.y) + row * p.hidden + c);
-  if (PAST)
-    __builtin_nontemporal_store(Word2{o[0], o[1]}, to);
-  else
-    *to = Word2{o[0], o[1]};
+  __builtin_memcpy(static_cast<int8_t*>(p.y) + row * p.hidden + c, o, 8);
 }
 __device__ __forceinline__ float int8_scale(uint32_t top) {
   return top < 0x7F800000u ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7FC00000u);
@@ -194,7 +184,7 @@ __device__ __forceinline__ float int8_scale(uint32_t top) {
 // row (or four), with the weights in registers and the next row's loads under
 // way while the row's sum goes through LDS.  Bound by memory: 4096 x 4096 bf16
 // with a residual 23 us, 5.8 TB/s (a copy runs at 4.9, reads alone at 5.4,
-// writes at 6.9), to MXFP4 20 us, 5.4 TB/s; fp32 53 us, 5.1 TB/s.  A single row
+// writes at 6.9), to MXFP4 21 us, 5.2 TB/s; fp32 53 us, 5.1 TB/s.  A single row
 // takes 3.2 us, of which 2.5 is what the smallest kernel takes.
 template <typename X, typename S, bool RES, typename O, int W, int V>
 __global__ __launch_bounds__(kWave*(W == 1 ? 4 : W)) void rmsnorm_kernel(NormParams p) {
@@ -289,9 +279,9 @@ __global__ __launch_bounds__(kWave*(W == 1 ? 4 : W)) void rmsnorm_kernel(NormPar
     for (int v = 0; v < V; ++v) {
       const int c = 8 * t + v * kSpan;
       if constexpr (kMx) {
-        store_mxfp4<kPast>(p, row, c, s[v]);
+        store_mxfp4(p, row, c, s[v]);
       } else if constexpr (kInt8) {
-        if (c < p.hidden) store_int8<kPast>(p, row, c, s[v], top);
+        if (c < p.hidden) store_int8(p, row, c, s[v], top);
       } else {
         Cols8<O> o;
 #pragma unroll
@@ -379,9 +369,9 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_long_kernel(NormParams p) 
     float n[8] = {};
     if (c < p.hidden) normed(c, n);
     if constexpr (kMx) {
-      store_mxfp4<false>(p, row, c, n);
+      store_mxfp4(p, row, c, n);
     } else if constexpr (kInt8) {
-      if (c < p.hidden) store_int8<false>(p, row, c, n, top);
+      if (c < p.hidden) store_int8(p, row, c, n, top);
     } else if (c < p.hidden) {
       Cols8<O> o;
 #pragma unroll
@@ -404,8 +394,8 @@ bool many_rows(int64_t n_rows, int hidden) {
   constexpr bool kBf16 = sizeof(X) == 2 && sizeof(S) == 2;
   return n_rows * hidden * (int64_t)sizeof(X) >= (kBf16 ? 5 << 20 : 3 << 20);
 }
-// Workgroups that share many rows: four a CU (4096 x 4096 to int8 23.0 us, three
-// a CU 24.4, two 31.9).
+// Workgroups that share many rows: four a CU (4096 x 4096 bf16 without a residual
+// 12.7 us, three a CU 13.4, two 15.8).
 constexpr int kGroups = 256 * 4;
 
 template <typename X, typename S, bool RES, typename O>
