@@ -734,7 +734,7 @@ __global__ __launch_bounds__(kWave* WT* WC) void product_tiled_kernel(ProductPar
           if (tok >= it.m) continue;
           if (j + 4 * N <= p.rows) {
             // past the caches, which the operands go through (4096 x 4096 x 4096 40.0 ->
-            // 39.3 us)
+            // 39.3 us; gate/up, rounding, down and combine of 4096 tokens 910 -> 865)
             if (past)
               __builtin_nontemporal_store(
                   u32x4{piece[i + k][0], piece[i + k][1], piece[i + k][2], piece[i + k][3]},
