@@ -506,7 +506,7 @@ __device__ __forceinline__ void keep_stored(Cols8<T>& r) {
 // / W rows at a time, of every NW gridDim.x / W, and the columns' part of
 // dweight stays in registers, so that a workgroup writes one part.  The next
 // rows are loaded while the sums of these go through the workgroup.  With
-//   dx = r w dy - s r^3 / hidden sum(s w dy)
+//   dx = r w dy - (s r) (r^2 / hidden sum(s w dy))
 // both sums take the one pass that r takes.  Bound by memory: 4096 x 4096 bf16
 // with dtotal 30 us (dx alone, without dtotal and dweight, 19 us, 5.2 TB/s);
 // dweight costs 5.5 us, the parts' join being a launch of its own.  fp32 57 us,
@@ -593,17 +593,18 @@ __global__ __launch_bounds__(kWave* NW) void rmsnorm_back_kernel(BackParams p) {
         keep_stored(s[v]);
       }
     const double r = rsqrt(ss * p.inv_hidden + p.eps);
-    const float rf = (float)r, k = (float)(r * r * r * sg * p.inv_hidden);
+    // s r is of order one whatever the size of the row, where r^3 may leave fp32
+    const float rf = (float)r, k = (float)(r * r * sg * p.inv_hidden);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       Cols8<S> o;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float di = static_cast<float>(d[v].v[i]), si = static_cast<float>(s[v].v[i]);
-        float g = rf * (w[v][i] * di) - k * si;
+        const float di = static_cast<float>(d[v].v[i]), n = static_cast<float>(s[v].v[i]) * rf;
+        float g = rf * (w[v][i] * di) - k * n;
         if (TOT) g += static_cast<float>(tot[v].v[i]);
         o.v[i] = static_cast<S>(g);
-        acc[v][i] += di * si * rf;
+        acc[v][i] += di * n;
       }
       store_own<(kRows > 1)>(static_cast<S*>(p.dx) + row * p.dx_stride,
                              Columns(c0 + v * kSpan, p.hidden), o);
@@ -676,7 +677,7 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParam
     sg += part[i][1];
   }
   const double r = rsqrt(ss * p.inv_hidden + p.eps);
-  const float rf = (float)r, k = (float)(r * r * r * sg * p.inv_hidden);
+  const float rf = (float)r, k = (float)(r * r * sg * p.inv_hidden);
   if (threadIdx.x == 0 && p.inv != nullptr) p.inv[row] = rf;
   for (int c = 8 * threadIdx.x; c < p.hidden; c += kNormBackCols) {
     const int m = p.hidden - c;
@@ -687,7 +688,7 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParam
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float w = i < m ? weight_at(p.weight, p.w_bf16, c + i) : 0.0f;
-      float g = rf * (w * static_cast<float>(d.v[i])) - k * static_cast<float>(v.v[i]);
+      float g = rf * (w * static_cast<float>(d.v[i])) - k * (static_cast<float>(v.v[i]) * rf);
       if (TOT) g += static_cast<float>(tv.v[i]);
       o.v[i] = static_cast<S>(g);
     }
@@ -703,7 +704,7 @@ __global__ __launch_bounds__(256) void rmsnorm_back_columns_kernel(BackParams p)
 #pragma unroll 4
   for (int64_t row = blockIdx.y; row < p.n_rows; row += gridDim.y)
     acc += static_cast<float>(static_cast<const D*>(p.dy)[row * p.dy_stride + c]) *
-           static_cast<float>(static_cast<const S*>(p.s)[row * p.s_stride + c]) * p.inv[row];
+           (static_cast<float>(static_cast<const S*>(p.s)[row * p.s_stride + c]) * p.inv[row]);
   p.dw[(int64_t)blockIdx.y * p.hidden + c] = acc;
 }
 

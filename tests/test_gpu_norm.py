@@ -4,8 +4,8 @@
 Bounds: the sum of squares and r are fp64.  Outputs in fp32 (and what is
 rounded further) are fp64 up to one rounding: half a step.  bf16 outputs are
 three fp32 roundings (r, the product with s, that with the weight) and one to
-bf16.  dx = rf (w dy) - k s + dtotal in fp32: three roundings in the first
-term, in the second one of k and one of the product beside the rounding of
+bf16.  dx = rf (w dy) - k (s rf) + dtotal in fp32: three roundings in the first
+term, in the second those of k, rf, s rf and the product beside the rounding of
 each w dy in k's sum, one for each of the two sums, then the output's.
 dweight: two products and the rounding of r a term, one rounding for each row
 that a wavefront adds, of the workgroup's part one, fp64 over the wavefronts
@@ -243,7 +243,7 @@ def _back_check(n, h, pad, dt, st, wt, total):
     g = wn * dn
     k = np.abs(r ** 3 * (sn * g).mean(axis=1, keepdims=True))
     kerr = U32 * (np.abs(sn * g).mean(axis=1, keepdims=True) * r ** 3 + k)
-    err = 3 * U32 * np.abs(r * g) + np.abs(sn) * (kerr + U32 * k)
+    err = 3 * U32 * np.abs(r * g) + np.abs(sn) * (kerr + 3 * U32 * k)
     sums = np.abs(r * g) + np.abs(k * sn) + (0 if tn is None else np.abs(tn) + np.abs(dx))
     err = (err + U32 * sums) * (1 + 2.0 ** -10)
     assert_within(got[0], dx, err + half_step(st) * (np.abs(dx) + err) + 2.0 ** -149, "dx")
@@ -309,6 +309,26 @@ def test_short_rows_of_more_than_a_launch():
     rows = -(-n // 64) + 1
     assert_within(dw, dwr, U32 * (6 + rows) * (f64(x) ** 2 * norm_ref(f64(x), 1.0, EPS)[1]).sum(0),
                   "dweight")
+
+
+@pytest.mark.parametrize("n,h", [(6, 1000), (700, 1000), (1600, 520), (6, 9000)])
+@pytest.mark.parametrize("scale", [2.0 ** 84, 2.0 ** 110, 2.0 ** -100])
+def test_gradients_of_far_rows(n, h, scale):
+    # r from 2^-110 to 2^10: squares, r^3 and dy s of large rows leave fp32.  dx
+    # of those is of the order of r; times 1 / r it is held to the bound of rows
+    # of order one (4 roundings of each of two terms and the sum, and the w dy
+    # in k's sum: 20 U32 of values below 64)
+    s, _, w = _inputs(n, h, F32, None, F32, h)
+    s = s * scale
+    dy = normal(3, n, h) * 64
+    dx, dw = B.moe_rmsnorm_backward(dy.cuda(), s.cuda(), w.cuda(), EPS)
+    want, dwr = norm_back_ref(f64(dy), f64(s), f64(w), EPS)
+    _, r = norm_ref(f64(s), f64(w), EPS)
+    size = np.abs(f64(w) * f64(dy)) + np.abs(f64(s) * r) * np.abs(
+        (f64(s) * r * f64(w) * f64(dy))).mean(axis=1, keepdims=True)
+    assert np.all(np.abs(f64(dx) - want) / r <= 20 * U32 * size + 2.0 ** -149 / r)
+    terms = np.abs(f64(dy) * f64(s) * r).sum(axis=0)
+    assert_within(dw, dwr, U32 * ((n + 9) * terms + np.abs(dwr)) + 2.0 ** -149, "dweight")
 
 
 def test_gradients_against_differences():
