@@ -207,3 +207,45 @@ def test_gathered_rows_past_four_gigabytes():
     assert not bool(out.any())
     del codes, scales, out
     torch.cuda.empty_cache()
+
+
+def test_tiled_products_in_a_graph_follow_their_inputs():
+    # one capture; the rows, the counts and the gather change between replays
+    n, k, e, rows, cols = 1100, 3, 24, 530, 1056
+    slots = n * k
+    gate, up = (B.Mxfp4Weight(*_random(i, e, rows, cols, mid=124)) for i in (1, 2))
+    down = B.Mxfp4Weight(*_random(3, e, 200, 32 * (rows // 32), mid=124))
+    assert B.moe_mxfp4_form(e, rows, cols, slots, True, True)[2] > 0
+    x = torch.randn(n, cols, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    offsets = torch.zeros(e + 1, dtype=torch.int32, device="cuda")
+    perm = torch.arange(slots, dtype=torch.int32, device="cuda")
+    g = (offsets[:e], offsets, perm, perm)
+
+    def deal(seed):
+        counts = np.random.default_rng(seed).multinomial(slots - 100 * seed, np.ones(e) / e)
+        counts[seed] = 0
+        offsets.copy_(torch.from_numpy(np.concatenate([[0], np.cumsum(counts)])).int())
+        perm.copy_(torch.randperm(slots, generator=torch.Generator().manual_seed(seed)).int())
+        x.copy_(torch.roll(x, 1, 0) * 1.25)
+
+    def passes():
+        h = B.moe_swiglu_mxfp4(gate, up, *B.moe_quantize_mxfp4(x), g, top_k=k)
+        h = h[:, :32 * (rows // 32)]
+        return h, B.moe_product_mxfp4(down, *B.moe_quantize_mxfp4(h), g, out_dtype=F32)
+
+    deal(1)
+    passes()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = passes()
+    for seed in range(4):
+        deal(seed)
+        want = [t.clone() for t in passes()]
+        for t in out:
+            t.fill_(3)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want)), seed
+        total = int(offsets[-1])
+        assert bool(want[1][:total].any()) and not bool(want[1][total:].any())
