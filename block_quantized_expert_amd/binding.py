@@ -740,6 +740,9 @@ def mxfp4_scale_rows(scales, cols):
     """Scale words [words][n][16], as moe_quantize_mxfp4 writes them, as scale
     bytes by rows [n][cols/32]: the order of moe.h's weights and of Mxfp4Weight's
     argument (a copy)."""
+    if scales.dim() != 3 or scales.shape[2] != 16 or 512 * scales.shape[0] < cols:
+        raise ValueError("scales must be words of shape (%d, n, 16), have %s"
+                         % (-(-cols // 512), tuple(scales.shape)))
     words, n, _ = scales.shape
     return scales.permute(1, 0, 2).reshape(n, words * 16)[:, :cols // 32].contiguous()
 

@@ -452,6 +452,15 @@ PyObject* rmsnorm_int8(Args a) {
   return results({&q, &scale, &v.total});
 }
 
+// Scale words of n rows of c columns.  The shape is looked at, not the size
+// alone: scale bytes by rows [n][c / 32] are as many where c is a multiple of 512.
+void scale_words_arg(const at::Tensor& t, int64_t n, int64_t c, c10::Device dev) {
+  const int64_t words = MOE_MXFP4_WORDS(c);
+  TORCH_CHECK_VALUE(t.dim() == 3 && t.size(0) == words && t.size(1) == n && t.size(2) == 16,
+                    "scales must be words of shape (", words, ", ", n, ", 16), have ", t.sizes());
+  dense_arg(t, "scales", at::kByte, words * n * 16, dev);
+}
+
 // Codes and scale words of n rows of c columns, given or new.
 struct Mxfp4Out {
   at::Tensor codes, scales;
@@ -461,7 +470,7 @@ struct Mxfp4Out {
     scales = given_scales != Py_None ? tensor(given_scales, "scales")
                                      : empty({words, n, 16}, at::kByte, dev);
     dense_arg(codes, "codes", at::kByte, n * (c / 2), dev);
-    dense_arg(scales, "scales", at::kByte, words * n * 16, dev);
+    scale_words_arg(scales, n, c, dev);
   }
 };
 
@@ -549,7 +558,7 @@ struct Mxfp4In {
     n = codes.size(0);
     cols = 2 * codes.size(1);
     dense_arg(codes, "codes", at::kByte, n * (cols / 2), dev);
-    dense_arg(scales, "scales", at::kByte, MOE_MXFP4_WORDS(cols) * n * 16, dev);
+    scale_words_arg(scales, n, cols, dev);
   }
 };
 
