@@ -696,16 +696,21 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParam
   }
 }
 
+// fp64: a thread adds a 64th of all rows, one after the other, and in fp32 the
+// roundings of rows alike add up (2^20 rows of 5 columns: 2e-4 of the sum; here
+// 2^-23).  No slower: 58 us of 4096 x 16384 bf16, 119 of fp32 with either.
 template <typename D, typename S>
 __global__ __launch_bounds__(256) void rmsnorm_back_columns_kernel(BackParams p) {
   const int c = blockIdx.x * 256 + threadIdx.x;
   if (c >= p.hidden) return;
-  float acc = 0;
+  double acc = 0;
 #pragma unroll 4
-  for (int64_t row = blockIdx.y; row < p.n_rows; row += gridDim.y)
-    acc += static_cast<float>(static_cast<const D*>(p.dy)[row * p.dy_stride + c]) *
-           (static_cast<float>(static_cast<const S*>(p.s)[row * p.s_stride + c]) * p.inv[row]);
-  p.dw[(int64_t)blockIdx.y * p.hidden + c] = acc;
+  for (int64_t row = blockIdx.y; row < p.n_rows; row += gridDim.y) {
+    const float d = static_cast<float>(static_cast<const D*>(p.dy)[row * p.dy_stride + c]);
+    const float s = static_cast<float>(static_cast<const S*>(p.s)[row * p.s_stride + c]);
+    acc = fma((double)d, (double)(s * p.inv[row]), acc);
+  }
+  p.dw[(int64_t)blockIdx.y * p.hidden + c] = (float)acc;
 }
 
 // dweight from the workgroups' parts: 32 columns a workgroup, whole lines of

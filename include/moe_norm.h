@@ -74,9 +74,10 @@ moe_status moe_rmsnorm_mxfp4(const moe_norm_rows* rows, uint8_t* codes, uint8_t*
  *   dx_j      = r g_j - s_j r^3 / hidden * sum_i s_i g_i + dtotal_j,
  *               which is the gradient of x and of the residual alike
  *   dweight_j = sum over the rows of dy_j s_j r
- * The sums along a row are taken in fp64, those over rows in fp32 by wavefront
- * and then in fp64, in an order that n_rows, hidden and the types fix: a call
- * repeats bit for bit.
+ * The sums along a row are taken in fp64.  Those over rows are fp32 within a
+ * wavefront, which adds up a 256th of the rows at most, and fp64 from there on;
+ * of more than 8192 columns, or fewer than eight, they are fp64 throughout.
+ * n_rows, hidden and the types fix their order: a call repeats bit for bit.
  *   dy       [n_rows][hidden] of dy_type.
  *   s        [n_rows][hidden] of s_type.
  *   dtotal   nullable, of s_type.
