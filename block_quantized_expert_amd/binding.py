@@ -751,7 +751,10 @@ class Mxfp4Weight:
     """A moe_mxfp4_weight over device tensors (kept alive): ``codes`` uint8
     [n_experts][rows][cols/2] or [rows][cols/2], ``scales`` uint8 with at least
     cols/32 bytes a row in place of cols/2 (moe.h's order; bytes past those are
-    not looked at).  The scales are laid out anew, once, here."""
+    not looked at).  The scales are laid out anew, once, here, on the current
+    stream of their device, which is waited for, so that a weight serves on any
+    stream (while that stream is captured, the layout becomes part of the graph
+    instead)."""
 
     def __init__(self, codes, scales):
         if codes.dim() == 2:
@@ -768,6 +771,10 @@ class Mxfp4Weight:
         by_row[:, :, :c // 32] = scales[:, :, :c // 32]
         self.codes = codes
         self.scales = by_row.view(e, r, words, 16).transpose(1, 2).contiguous()
+        if codes.is_cuda:
+            with torch.cuda.device(codes.device):
+                if not torch.cuda.is_current_stream_capturing():
+                    torch.cuda.current_stream().synchronize()
         self.c = MoeMxfp4Weight(e, r, c, codes.data_ptr(), self.scales.data_ptr())
         self.address = ctypes.addressof(self.c)
 
