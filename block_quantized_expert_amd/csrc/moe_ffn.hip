@@ -44,6 +44,7 @@
 #include "moe_device.h"
 #include "moe_formats.h"
 #include "moe_kernels.h"
+#include "moe_launch.h"
 
 namespace moe {
 namespace {
@@ -1023,13 +1024,6 @@ hipError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t lds,
   return e != hipSuccess ? e : hipGetLastError();
 }
 
-// Kernels that ask for more than 64 KiB of dynamic LDS say so once.
-template <typename K>
-hipError_t allow_lds(K kernel) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBudget);
-}
-
 // fp32 activations: bf16 ones take the grouped GEMM or the decode kernel,
 // so only the XF32 instantiations are launched.
 template <int NBT>
@@ -1041,7 +1035,7 @@ hipError_t gate_up_launch(const FfnParams& p, dim3 grid, hipStream_t stream, hip
     const int rows = p.n_tokens < 16 ? p.n_tokens : 16;
     const size_t lds = (size_t)rows * x_stride;
     if (lds <= (size_t)kLdsBudget) {
-      static const hipError_t attr = allow_lds(gate_up_kernel<1, true, true>);
+      const hipError_t attr = allow_lds<gate_up_kernel<1, true, true>, kLdsBudget>();
       if (attr != hipSuccess) return attr;
       return launch(gate_up_kernel<1, true, true>, grid, dim3(kThreads), lds, stream, start,
                     stop, p, x_stride);
@@ -1075,7 +1069,7 @@ hipError_t down_small_launch(const FfnParams& p, int slots, hipStream_t stream, 
   const int zero_row = kStageRow * 2;
   int spc = (kLdsBudget - zero_row) / per_step;
   spc = spc < 1 ? 1 : (spc > nks ? nks : spc);
-  static const hipError_t attr = allow_lds(down_combine_small_kernel<WT, SWT>);
+  const hipError_t attr = allow_lds<down_combine_small_kernel<WT, SWT>, kLdsBudget>();
   if (attr != hipSuccess) return attr;
   return launch(down_combine_small_kernel<WT, SWT>, dim3(p.hidden / 16), dim3(kSmallThreads),
                 (size_t)spc * per_step + zero_row, stream, start, stop, p, spc);
@@ -1092,15 +1086,15 @@ hipError_t gate_up_decode_launch(const FfnParams& p, hipStream_t stream, hipEven
   const int m_max = p.n_tokens < kDecodeMaxTokens ? p.n_tokens : kDecodeMaxTokens;
   const size_t lds = (size_t)kWaves * m_max * (S * 128 + 8) * 2;
   if (p.lazy_tau == 0.0f) {
-    static const hipError_t attr = allow_lds(gate_up_decode_kernel<S, 0>);
+    const hipError_t attr = allow_lds<gate_up_decode_kernel<S, 0>, kLdsBudget>();
     if (attr != hipSuccess) return attr;
     return launch(gate_up_decode_kernel<S, 0>, dim3(blocks), dim3(kThreads), lds, stream, start,
                   stop, p, a_bound, m_max);
   }
   // gate first: the routed gate rows, then the up rows of the experts some
   // token keeps, and the shared expert
-  static const hipError_t attr1 = allow_lds(gate_up_decode_kernel<S, 1>);
-  static const hipError_t attr2 = allow_lds(gate_up_decode_kernel<S, 2>);
+  const hipError_t attr1 = allow_lds<gate_up_decode_kernel<S, 1>, kLdsBudget>();
+  const hipError_t attr2 = allow_lds<gate_up_decode_kernel<S, 2>, kLdsBudget>();
   if (attr1 != hipSuccess) return attr1;
   if (attr2 != hipSuccess) return attr2;
   hipError_t e = launch(gate_up_decode_kernel<S, 1>, dim3(routed > 0 ? routed : 1),

@@ -53,6 +53,7 @@
 #include "moe_device.h"
 #include "moe_formats.h"
 #include "moe_kernels.h"
+#include "moe_launch.h"
 
 namespace moe {
 namespace {
@@ -1866,12 +1867,6 @@ hipError_t launch(void (*kernel)(Params...), dim3 grid, dim3 block, size_t lds,
   return e != hipSuccess ? e : hipGetLastError();
 }
 
-template <typename K>
-hipError_t allow_lds(K kernel) {
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, kGemmLds);
-}
-
 // Upper bound on the items of segments seg_lo .. seg_hi-1: routed token
 // tiles number at most N*k/TT + min(E, N*k); the shared expert has
 // ceil(N/TT).
@@ -1912,7 +1907,7 @@ int grid_for(int64_t items) {
 template <int WT, int TT, bool SC, bool O32, bool LAZY, bool PK, bool H6>
 hipError_t gate_up_range_as(const FfnParams& p, int seg_lo, int seg_hi, hipStream_t stream,
                             hipEvent_t start, hipEvent_t stop) {
-  static const hipError_t attr = allow_lds(gemm_gate_up_kernel<WT, TT, SC, O32, LAZY, PK, H6>);
+  const hipError_t attr = allow_lds<gemm_gate_up_kernel<WT, TT, SC, O32, LAZY, PK, H6>, kGemmLds>();
   if (attr != hipSuccess) return attr;
   const int grid = grid_for(items_bound(p, seg_lo, seg_hi, TT, kGuRows, false));
   return launch(gemm_gate_up_kernel<WT, TT, SC, O32, LAZY, PK, H6>, dim3(grid), dim3(kGThreads),
@@ -1923,7 +1918,7 @@ hipError_t gate_up_range_as(const FfnParams& p, int seg_lo, int seg_hi, hipStrea
 template <bool LAZY>
 hipError_t gate_up_mix_as(const FfnParams& p, hipStream_t stream, hipEvent_t start,
                           hipEvent_t stop) {
-  static const hipError_t attr = allow_lds(gemm_gate_up_mix_kernel<LAZY>);
+  const hipError_t attr = allow_lds<gemm_gate_up_mix_kernel<LAZY>, kGemmLds>();
   if (attr != hipSuccess) return attr;
   const int grid = grid_for(items_bound(p, 0, p.n_experts + 1, 64, kGuRows, false));
   return launch(gemm_gate_up_mix_kernel<LAZY>, dim3(grid), dim3(kGThreads), (size_t)kGemmLds,
@@ -1942,9 +1937,7 @@ template <bool MIX>
 hipError_t down6_range(const FfnParams& p, int seg_lo, int seg_hi, hipStream_t stream,
                        hipEvent_t start, hipEvent_t stop) {
   constexpr int lds = MIX && kD3Lds > kD6Lds ? kD3Lds : kD6Lds;
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(gemm_down6_kernel<MIX>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  const hipError_t attr = allow_lds<gemm_down6_kernel<MIX>, lds>();
   if (attr != hipSuccess) return attr;
   const int grid = grid_for(items_bound(p, seg_lo, seg_hi, kD3Tok, kDnRows, true));
   return launch(gemm_down6_kernel<MIX>, dim3(grid), dim3(kGThreads), (size_t)lds, stream, start,
@@ -1954,9 +1947,7 @@ hipError_t down6_range(const FfnParams& p, int seg_lo, int seg_hi, hipStream_t s
 template <int WT, bool SC, bool PK = false>
 hipError_t down3_range(const FfnParams& p, int seg_lo, int seg_hi, hipStream_t stream,
                        hipEvent_t start, hipEvent_t stop) {
-  static const hipError_t attr =
-      hipFuncSetAttribute(reinterpret_cast<const void*>(gemm_down3_kernel<WT, SC, PK>),
-                          hipFuncAttributeMaxDynamicSharedMemorySize, kD3Lds);
+  const hipError_t attr = allow_lds<gemm_down3_kernel<WT, SC, PK>, kD3Lds>();
   if (attr != hipSuccess) return attr;
   const int grid = grid_for(items_bound(p, seg_lo, seg_hi, kD3Tok, kDnRows, true));
   return launch(gemm_down3_kernel<WT, SC, PK>, dim3(grid), dim3(kGThreads), (size_t)kD3Lds,
@@ -1966,7 +1957,7 @@ hipError_t down3_range(const FfnParams& p, int seg_lo, int seg_hi, hipStream_t s
 template <int WT, int TT, bool SC>
 hipError_t down_range(const FfnParams& p, int seg_lo, int seg_hi, hipStream_t stream,
                       hipEvent_t start, hipEvent_t stop) {
-  static const hipError_t attr = allow_lds(gemm_down_kernel<WT, TT, SC>);
+  const hipError_t attr = allow_lds<gemm_down_kernel<WT, TT, SC>, kGemmLds>();
   if (attr != hipSuccess) return attr;
   const int grid = grid_for(items_bound(p, seg_lo, seg_hi, TT, kDnRows, true));
   return launch(gemm_down_kernel<WT, TT, SC>, dim3(grid), dim3(kGThreads), (size_t)kGemmLds,

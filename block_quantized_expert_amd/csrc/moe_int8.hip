@@ -8,6 +8,7 @@
 
 #include "moe_device.h"
 #include "moe_grouped.h"
+#include "moe_launch.h"
 #include "moe_ops_host.h"
 #include "moe_probe.h"
 #include "moe_round.h"
@@ -632,9 +633,8 @@ hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) 
   static_assert(L::kBytes <= 160 * 1024, "LDS");
   static_assert(L::kMinSteps == 1 || (TOK == 128 && CH == 256), "steps");
   constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
-  static const hipError_t attr = hipFuncSetAttribute(
-      reinterpret_cast<const void*>(kernel), hipFuncAttributeMaxDynamicSharedMemorySize, L::kBytes);
-  if (attr != hipSuccess) return attr;
+  const hipError_t e = allow_lds<kernel, L::kBytes>();
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3(kCus * per_cu), dim3(kWave * WT * WC), L::kBytes, stream, p);
   return hipGetLastError();
 }

@@ -4,11 +4,11 @@
 
 #include <math.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "moe_device.h"
 #include "moe_grouped.h"
+#include "moe_launch.h"
 #include "moe_mxfp4.h"
 #include "moe_ops_host.h"
 #include "moe_probe.h"
@@ -796,16 +796,7 @@ hipError_t launch_tiled(const ProductParams& p, int per_cu, hipStream_t stream) 
   using L = TiledLds<TOK, CH, WT * WC, STAGES>;
   static_assert(L::bytes(MOE_MAX_EXPERTS) <= kMaxLds || (TOK == 128 && CH == 256), "LDS");
   constexpr auto kernel = product_tiled_kernel<SWIGLU, O, TOK, CH, WT, WC, STAGES>;
-  // once for each device
-  static std::atomic<uint64_t> allowed{0};
-  int device = 0;
-  hipError_t e = hipGetDevice(&device);
-  const uint64_t bit = uint64_t{1} << (device & 63);
-  if (e == hipSuccess && (allowed.load(std::memory_order_relaxed) & bit) == 0) {
-    e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                            hipFuncAttributeMaxDynamicSharedMemorySize, kMaxLds);
-    if (e == hipSuccess) allowed.fetch_or(bit, std::memory_order_relaxed);
-  }
+  const hipError_t e = allow_lds<kernel, kMaxLds>();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3(kCus * per_cu), dim3(kWave * WT * WC), L::bytes(p.n_experts),
                      stream, p);
