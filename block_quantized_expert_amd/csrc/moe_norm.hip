@@ -427,7 +427,7 @@ hipError_t launch_norm(NormParams p, hipStream_t stream) {
   else if (many && vectors <= 4 * kWave * V)
     launch(rmsnorm_kernel<X, S, RES, O, 4, V>, n, 4);
   else if (V == 2 && many)  // fp32 rows: 4096 x 5120 31.1 us, 8192 columns 52.1 (V 1: 43.0, 61.3)
-    launch(rmsnorm_kernel<X, S, RES, O, 8, 2>, n, 8);
+    launch(rmsnorm_kernel<X, S, RES, O, 8, V == 2 ? 2 : 1>, n, 8);  // (V 4 ends above)
   else if (vectors <= 4 * kWave)
     launch(rmsnorm_kernel<X, S, RES, O, 4, 1>, n, 4);
   else if (vectors <= 8 * kWave)
