@@ -8,6 +8,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -45,6 +46,7 @@ class RouteWeights(torch.autograd.Function):
         return (w,) + grouping
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dw, *_):
         logits, ids = ctx.saved_tensors
         return B.moe_route_backward(logits, ids, dw.contiguous(), ctx.routed_scale), None, None
@@ -58,6 +60,7 @@ class Dispatch(torch.autograd.Function):
         return B.moe_dispatch(x, grouping, top_k)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, drows):
         dx = B.moe_dispatch_backward(drows.contiguous(), ctx.saved_tensors, ctx.top_k)
         return (dx, None) + (None,) * 4
@@ -70,6 +73,7 @@ class Combine(torch.autograd.Function):
         return B.moe_combine(rows, w, grouping)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy):
         rows, w, *grouping = ctx.saved_tensors
         drows, dw = B.moe_combine_backward(dy.contiguous(), rows, w, tuple(grouping))

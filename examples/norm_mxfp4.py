@@ -8,6 +8,7 @@ import os
 import sys
 
 import torch
+from torch.autograd.function import once_differentiable
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
@@ -52,6 +53,7 @@ class AddNorm(torch.autograd.Function):
         return y, total
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, dtotal):
         total, weight = ctx.saved_tensors
         d, dw = B.moe_rmsnorm_backward(dy.contiguous(), total, weight, ctx.eps,
