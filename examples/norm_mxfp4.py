@@ -56,9 +56,11 @@ class AddNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, dy, dtotal):
         total, weight = ctx.saved_tensors
-        d, dw = B.moe_rmsnorm_backward(dy.contiguous(), total, weight, ctx.eps,
-                                       dtotal=dtotal.contiguous())
-        return d.to(ctx.types[0]), d.to(ctx.types[1]), dw.to(weight.dtype), None
+        want = ctx.needs_input_grad[2]  # not of a frozen weight
+        d = B.moe_rmsnorm_backward(dy.contiguous(), total, weight, ctx.eps,
+                                   dtotal=dtotal.contiguous(), need_dweight=want)
+        d, dw = (d[0], d[1].to(weight.dtype)) if want else (d, None)
+        return d.to(ctx.types[0]), d.to(ctx.types[1]), dw, None
 
 
 def main():

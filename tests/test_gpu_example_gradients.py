@@ -1,11 +1,13 @@
 """The examples' autograd functions: a second derivative, which the calls do not
-have, is refused instead of left out."""
+have, is refused instead of left out; gradients that nobody wants are not taken."""
 
 import importlib.util
 import os
 
 import pytest
 import torch
+
+from block_quantized_expert_amd import binding as B
 
 pytestmark = pytest.mark.gpu
 
@@ -36,6 +38,28 @@ def test_add_norm_refuses_second_derivatives(of):
     assert all(torch.equal(a, b) for a, b in zip(grads, plain))
     with pytest.raises(RuntimeError, match="once_differentiable"):
         grads[0].square().sum().backward()
+
+
+@pytest.mark.parametrize("frozen", [False, True])
+def test_add_norm_takes_the_weights_gradient_where_it_is_wanted(frozen, monkeypatch):
+    example = _load("norm_mxfp4")
+    x, r = _normal(1, 5, 96).requires_grad_(), _normal(2, 5, 96).requires_grad_()
+    w = (1 + 0.2 * _normal(3, 96)).requires_grad_(not frozen)
+    asked = []
+    call = B.moe_rmsnorm_backward
+
+    def seen(*args, **kw):
+        asked.append(kw.get("need_dweight", True))
+        return call(*args, **kw)
+
+    monkeypatch.setattr(B, "moe_rmsnorm_backward", seen)
+    y, total = example.AddNorm.apply(x, r, w, 1e-6)
+    (y * _normal(4, 5, 96) + total).sum().backward()
+    assert asked == [not frozen] and (w.grad is None) == frozen
+    s = (x + r).detach()
+    dx = call(_normal(4, 5, 96), s, w.detach(), 1e-6, dtotal=torch.ones_like(s),
+              need_dweight=False)
+    assert torch.equal(x.grad, dx) and torch.equal(r.grad, dx)
 
 
 def test_experts_around_refuse_second_derivatives():
