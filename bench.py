@@ -10,16 +10,18 @@ prefill of 4096 tokens on the DeepSeek-V4-Flash-shaped layer (hidden 4096,
 256 routed MXFP4 experts + 1 fp8-e4m3 shared, intermediate 2048, top-6).
 Its K timed steps follow W warm-up steps.  The other workloads (tiny,
 single-token decode, batched decode of 32, prefill of 512) are measured in
-the same run, each with its own step count, and reported as nested records
-under "configs", together with records of the routing and FFN options
-(VARIANTS: tail pruning, group-limited top-k, the gate-first lazy skip) on
-those workloads (``--workload NAME`` measures only that one as the line).
+the same run, each with its own step count, and reported under "configs",
+together with the routing and FFN options (VARIANTS: tail pruning,
+group-limited top-k, the gate-first lazy skip) on those workloads
+(``--workload NAME`` measures only that one as the line).  There they are in
+brief, so that the line stays a few KB and is not cut where output is kept by
+its end; ``--records FILE`` writes it with these records in full.
 
 Cold caches: the weights live in several independent layer copies (3.44 GB
 each) used round-robin, and every step takes a fresh batch from a seeded
 pool, so no expert is served from the 256 MB last-level cache or the L2s.
 
-Every record holds:
+Every record in full holds:
 - ``value``: tokens/s over its timed steps (wall clock, synchronised on both
   sides) and ``ms_per_step``;
 - ``step_stats``: the timed steps split into five consecutive repetitions,
@@ -609,6 +611,20 @@ def mfma_ceiling(dev, iters=8000, reps=5):
             "TFLOPs": res, "fp8_peak_TFLOPs": 5000.0}
 
 
+def brief(rec):
+    """The figures of a record that the line carries under "configs"."""
+    r = rec["roofline"]
+    out = {"value": round(rec["value"], 1), "ms_per_step": round(rec["ms_per_step"], 6),
+           "steps": rec["steps"], "warmup": rec["warmup"],
+           "roofline": {"bound": r["bound"], "frac": round(r["frac"], 4),
+                        "avg_launch_us": round(r["avg_launch_us"], 2)},
+           "hbm_frac": round(rec["path"]["hbm_frac"], 4),
+           "mfma_bf16_frac": round(rec["path"]["mfma_bf16_frac"], 4)}
+    if "cpu_baseline" in rec:
+        out["cpu_tokens_per_s"] = round(rec["cpu_baseline"]["value"], 3)
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -616,7 +632,7 @@ def main():
     ap.add_argument("--warmup", type=int, default=None)
     ap.add_argument("--workload", default=None,
                     help="measure only this workload (default: %s as the line, the others "
-                         "as nested records)" % HEADLINE)
+                         "under configs)" % HEADLINE)
     ap.add_argument("--copies", type=int, default=None)
     ap.add_argument("--pool", type=int, default=None)
     ap.add_argument("--no-cpu-baseline", action="store_true")
@@ -630,6 +646,8 @@ def main():
                          "copy kernel (a known byte count for calibrating memory counters)")
     ap.add_argument("--cpu-seconds", type=float, default=15.0)
     ap.add_argument("--nested-cpu-seconds", type=float, default=4.0)
+    ap.add_argument("--records", default=None, metavar="FILE",
+                    help="write the line there with the records under configs in full")
     args = ap.parse_args()
     global PACK
     PACK = not args.no_pack
@@ -713,8 +731,11 @@ def main():
     if not args.no_ceiling:
         result["hbm_read_ceiling"] = read_ceiling(dev)
         result["mfma_issue_ceiling"] = mfma_ceiling(dev)
+    if args.records:
+        with open(args.records, "w") as f:
+            json.dump(dict(result, configs=configs), f)
     if configs:
-        result["configs"] = configs
+        result["configs"] = {name: brief(c) for name, c in configs.items()}
     print(json.dumps(result), flush=True)
 
 
