@@ -574,9 +574,9 @@ def moe_forward_ex(layer: Layer, logits, x, opts, routed_scale=1.5,
 # ----------------------------------------------------------------------------
 # Rows in expert order, gradients of routing (moe_rows.h), products in 8-bit
 # integers (moe_int8.h), the RMS norm (moe_norm.h) and MXFP4 rows and products
-# (moe_mxfp4.h).  These calls check dtypes, shapes and layouts of their tensors (ValueError) on top of the library's own checks; outputs that are
-# not given are allocated on the call's stream.  csrc/tensor_calls.cpp holds
-# the checks.
+# (moe_mxfp4.h).  These calls check dtypes, shapes and layouts of their tensors
+# (ValueError) on top of the library's own checks; outputs that are not given
+# are allocated on the call's stream.  csrc/tensor_calls.cpp holds the checks.
 #
 # Like the calls above they are not recorded by autograd: an output never
 # requires a gradient, whatever the inputs do.  examples/experts_around.py puts

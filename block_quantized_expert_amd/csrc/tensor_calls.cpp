@@ -1,8 +1,8 @@
 // The calls of moe_rows.h, moe_int8.h, moe_norm.h and moe_mxfp4.h on torch
-// tensors: argument checks, outputs, the current stream, the C entry.  Their kernels take a few
-// microseconds at the size of one token, where the same steps in Python took
-// three times that (one token's combine, submission: 14 us through ctypes);
-// binding.py holds the signatures and the documentation.
+// tensors: argument checks, outputs, the current stream, the C entry.  Their
+// kernels take a few microseconds at the size of one token, where the same steps
+// in Python took three times that (one token's combine, submission: 14 us through
+// ctypes); binding.py holds the signatures and the documentation.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
