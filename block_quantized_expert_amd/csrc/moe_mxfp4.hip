@@ -390,12 +390,12 @@ __device__ __forceinline__ void swap8(uint32_t& a, uint32_t& b) {
 // What bounds it: for 4096 x 4096 x 4096 (38 us, 3.6 PFLOP/s; the instruction
 // alone 8.5) its steps and the clock.  The matrix cores are busy 33 thousand
 // cycles of some 77, LDS with operand reads 19 (3 of them bank conflicts) and
-// with the copies about 8, so neither is full: two stages, and a barrier for
-// every 32 instructions of a wavefront, leave the rest.  The card's power takes
-// the clock to 2.0 GHz on top: codes that are all zero, the same instructions,
-// take 32 us.  For experts' weights of 2.3 GB HBM (256 experts' gate and up of 2048 x 4096: 357
-// us for 512 tokens, 6.4 TB/s), and for 4096 tokens, 96 rows an expert, both
-// (475 us, 4.8 TB/s and 1.7 PFLOP/s).
+// with the copies about 8, so neither is full: what remains is the steps' own,
+// two stages and a barrier for every 32 instructions of a wavefront.  The card's
+// power takes the clock to 2.0 GHz on top: codes that are all zero, the same
+// instructions, take 32 us.  For experts' weights of 2.3 GB it is HBM (256
+// experts' gate and up of 2048 x 4096: 357 us for 512 tokens, 6.4 TB/s), and for
+// 4096 tokens, 96 rows an expert, both (475 us, 4.8 TB/s and 1.7 PFLOP/s).
 //   - Copies between the products, one every unit or two, not all in front: a
 //     wavefront waits at a copy's issue while the CU has many lines in flight.
 //   - Three stages of 128 x 256 tiles, four of the smaller ones, are as many as

@@ -705,7 +705,7 @@ __global__ __launch_bounds__(16 * kWave) void rmsnorm_back_long_kernel(BackParam
 
 // fp64: a thread adds a 64th of all rows, one after the other, and in fp32 the
 // roundings of rows alike add up (2^20 rows of 5 columns: 2e-4 of the sum; here
-// 2^-23).  No slower: 58 us of 4096 x 16384 bf16 with either.
+// 2^-22 at most).  No slower: 58 us of 4096 x 16384 bf16 with either.
 template <typename D, typename S>
 __global__ __launch_bounds__(256) void rmsnorm_back_columns_kernel(BackParams p) {
   const int c = blockIdx.x * 256 + threadIdx.x;

@@ -76,7 +76,8 @@ moe_status moe_rmsnorm_mxfp4(const moe_norm_rows* rows, uint8_t* codes, uint8_t*
  *   dweight_j = sum over the rows of dy_j s_j r
  * The sums along a row are taken in fp64.  Those over rows are fp32 within a
  * wavefront, which adds up a 256th of the rows at most, and fp64 from there on;
- * of more than 8192 columns, or fewer than eight, they are fp64 throughout.
+ * of more than 8192 columns, or fewer than eight, they are fp64 but for one
+ * rounding of each of 64 parts.
  * n_rows, hidden and the types fix their order: a call repeats bit for bit.
  *   dy       [n_rows][hidden] of dy_type.
  *   s        [n_rows][hidden] of s_type.
